@@ -6,7 +6,8 @@ package does not need a GPU, but every call does, and the library must have been
 (``python -m long_context_sparse_idx16_b200.build``): there is no fallback of any kind.
 
 The module-level functions carry the C names (rtp_create, rtp_append_kv, rtp_decode,
-rtp_prefill_chunk, rtp_destroy, ...); ``Layer`` wraps them for torch tensors.
+rtp_prefill_chunk, rtp_destroy, ...); ``Layer`` wraps them for torch tensors.  ``PagedKV``
+wraps the operators over a caller-owned paged cache (include/rtp_paged.h).
 """
 from __future__ import annotations
 
@@ -59,6 +60,14 @@ class rtp_cluster_view(C.Structure):
                 ("assign_stride", C.c_int64)]
 
 
+class rtp_paged_kv(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_stride", C.c_int64 * 3), ("v_stride", C.c_int64 * 3),
+                ("n_pages", C.c_int64), ("page_size", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("dtype", C.c_int32), ("k_scale", C.c_float), ("v_scale", C.c_float),
+                ("block_table", C.c_void_p), ("table_stride", C.c_int64), ("max_pages", C.c_int32),
+                ("n_seqs", C.c_int32), ("bounds", C.c_void_p), ("err", C.c_void_p)]
+
+
 class _DeviceArray:
     """A borrowed device array described by __cuda_array_interface__ (viewed by torch, no copy)."""
 
@@ -85,6 +94,7 @@ def lib() -> C.CDLL:
                               "`python -m long_context_sparse_idx16_b200.build`")
         L = C.CDLL(LIB_PATH)
         P, i32, i64, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_float
+        K = C.POINTER(rtp_paged_kv)
         sigs = {
             "rtp_create": ([C.POINTER(rtp_config), C.POINTER(C.c_void_p)], C.c_int),
             "rtp_destroy": ([P], C.c_int),
@@ -110,6 +120,17 @@ def lib() -> C.CDLL:
             "rtp_cluster_drop": ([P], C.c_int),
             "rtp_cluster_len": ([P, i32], i64),
             "rtp_get_clusters": ([P, C.POINTER(rtp_cluster_view)], C.c_int),
+            "rtp_paged_append": ([K, P, P, P, i32, i64, i64, i64, i32, i32, P, i32, P, P, P, P, f32, C.c_double, P,
+                                  i64, P, i64, P], C.c_int),
+            "rtp_paged_bounds": ([K, P, P], C.c_int),
+            "rtp_paged_decode": ([K, P, i32, i64, i32, i32, P, P, i32, i32, f32, P, P, i64, P, i64, P, P, i64, P,
+                                  C.c_size_t, P], C.c_int),
+            "rtp_paged_decode_workspace": ([K, i32, i32, C.c_int], C.c_size_t),
+            "rtp_paged_select": ([K, P, i32, i64, i32, i32, P, P, i32, i32, i32, P, i64, P, P, C.c_size_t, P],
+                                 C.c_int),
+            "rtp_paged_select_workspace": ([K, i32, i32], C.c_size_t),
+            "rtp_paged_evict": ([K, P, i32, i32, i32, P, P, i64, P, P, P, P, C.c_size_t, P], C.c_int),
+            "rtp_paged_evict_workspace": ([K, i64], C.c_size_t),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -472,3 +493,6 @@ class Layer:
         asg = torch.as_tensor(_DeviceArray(v.assign, (B, Hr, v.assign_stride), "<i2"), device=self.device)
         asg = asg[:, :, :v.max_seq].to(torch.int32) & 0xFFFF
         return {"centres": cent, "counts": counts, "assign": asg, "ready": bool(v.ready)}
+
+
+from .paged import PagedKV  # noqa: E402,F401  (needs the definitions above)
