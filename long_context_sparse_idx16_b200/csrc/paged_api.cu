@@ -23,8 +23,8 @@ const char* view_of(const rtp_paged_kv* kv, PagedView* p) {
   if (kv->n_kv_heads < 1 || kv->n_kv_heads > 1024) return "need 1 <= n_kv_heads <= 1024";
   if (kv->n_pages < 1 || kv->n_pages > 0x7fffffffLL) return "need 1 <= n_pages < 2^31";
   if (kv->n_seqs < 1 || kv->n_seqs > 65535) return "need 1 <= n_seqs <= 65535";
-  if (kv->max_pages < 1 || (int64_t)kv->max_pages * kv->page_size >= 0x7fffffffLL)
-    return "need max_pages >= 1 and fewer than 2^31 slots in a table row";
+  if (kv->max_pages < 1 || (int64_t)kv->max_pages * kv->page_size > 0x7fff0000LL)
+    return "need max_pages >= 1 and at most 2^31 - 2^16 slots in a table row";
   if (kv->table_stride < kv->max_pages) return "table_stride must be at least max_pages";
   if (!(kv->k_scale > 0.f) || !(kv->v_scale > 0.f) || !isfinite(kv->k_scale) || !isfinite(kv->v_scale))
     return "k_scale and v_scale must be positive and finite";
