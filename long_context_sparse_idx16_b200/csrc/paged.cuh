@@ -7,8 +7,11 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
+#include <type_traits>
 
+#include "mma_tile.cuh"
 #include "rtp_device.cuh"
 #include "rtp_internal.h"
 #include "rtp_paged.h"
@@ -79,6 +82,37 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
 template <>
 __device__ __forceinline__ __nv_fp8_e4m3 from_f32<__nv_fp8_e4m3>(float x) {
   return __nv_fp8_e4m3(x);  // nearest, saturating at 448, NaN kept
+}
+
+// ---- products on the tensor cores, fp16 or bf16 operands
+
+template <typename T>
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same_v<T, __half>)
+    mma16816(c, a, b0, b1);
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (std::is_same_v<T, __half>) return pack_half2(x, y);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// two e4m3 values (low 16 bits) as two T, exactly
+template <typename T>
+__device__ __forceinline__ uint32_t widen2(uint32_t x) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
+  const __half2 y = *reinterpret_cast<const __half2*>(&h);
+  if constexpr (std::is_same_v<T, __half>) return *reinterpret_cast<const uint32_t*>(&y);
+  const float2 f = __half22float2(y);
+  return pack2<T>(f.x, f.y);
 }
 
 // Order-preserving map of a double to 64 bits: equal values (0 and -0 among them) get equal keys,
@@ -221,8 +255,13 @@ struct SelectPagesArgs {
   int32_t* sel;
   int64_t sel_stride;
   int32_t* sel_count;
-  unsigned long long* keys;  // workspace [n_rows][Hkv][max_pages]
+  unsigned long long* keys;  // workspace [n_rows][Hkv][max_pages]: exact keys, where many are needed
+  float* approx;             // workspace [n_rows][Hkv][max_pages]
+  float* chunk_max;          // workspace [n_rows][Hkv][page_chunks(max_pages)]
 };
+// pages that one CTA of the page scoring takes
+constexpr int kPageChunk = 256;
+inline int page_chunks(int max_pages) { return (max_pages + kPageChunk - 1) / kPageChunk; }
 
 struct EvictArgs {
   PagedView kv;
@@ -235,8 +274,37 @@ struct EvictArgs {
   float* out_scores;
   int32_t* out_positions;
   int32_t* out_len;
-  int32_t* moves;  // workspace [n_seqs][Hkv][stride]: slots that move, then the slots they fill
+  int32_t* moves;   // workspace [n_seqs][Hkv][stride]: slots that move, then the slots they fill
+  int32_t* n_moves; // workspace [n_seqs][Hkv]
 };
+
+// Launch that may start while the kernel before it drains; it waits (griddepcontrol.wait) before
+// it reads what that kernel wrote.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, fn, args...);
+}
+
+// Dynamic shared memory of a kernel raised to `bytes`, once per device.
+template <typename Fn>
+cudaError_t allow_smem(Fn* fn, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+  return e;
+}
 
 cudaError_t launch_paged_append(const AppendArgs& a, int io_dtype, int kv_dtype, cudaStream_t st);
 cudaError_t launch_paged_bounds(const PagedView& kv, int kv_dtype, const int32_t* seq_len, cudaStream_t st);

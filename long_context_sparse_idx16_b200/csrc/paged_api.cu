@@ -207,7 +207,9 @@ rtp_status rtp_paged_decode(const rtp_paged_kv* kv, const void* q, int32_t q_dty
 
 size_t rtp_paged_select_workspace(const rtp_paged_kv* kv, int32_t n_rows, int32_t n_q_heads) {
   if (view_of(kv, nullptr) || n_rows < 1 || n_rows > 65535 || n_q_heads < 1) return 0;
-  return (size_t)n_rows * kv->n_kv_heads * kv->max_pages * sizeof(unsigned long long);
+  return (size_t)n_rows * kv->n_kv_heads *
+         ((size_t)kv->max_pages * (sizeof(unsigned long long) + sizeof(float)) +
+          (size_t)page_chunks(kv->max_pages) * sizeof(float));
 }
 
 rtp_status rtp_paged_select(const rtp_paged_kv* kv, const void* q, int32_t q_dtype, int64_t q_stride,
@@ -240,13 +242,16 @@ rtp_status rtp_paged_select(const rtp_paged_kv* kv, const void* q, int32_t q_dty
   a.sel_stride = sel_stride;
   a.sel_count = sel_count;
   a.keys = static_cast<unsigned long long*>(workspace);
+  const size_t lists = (size_t)n_rows * kv->n_kv_heads * kv->max_pages;
+  a.approx = reinterpret_cast<float*>(a.keys + lists);
+  a.chunk_max = a.approx + lists;
   const cudaError_t e = launch_paged_select(a, q_dtype, kv->dtype, stream);
   return e == cudaSuccess ? RTP_OK : cuda_fail(nullptr, e, fn);
 }
 
 size_t rtp_paged_evict_workspace(const rtp_paged_kv* kv, int64_t stride) {
   if (view_of(kv, nullptr) || stride < 1 || stride > (1 << 24)) return 0;
-  return (size_t)kv->n_seqs * kv->n_kv_heads * stride * sizeof(int32_t);
+  return (size_t)kv->n_seqs * kv->n_kv_heads * (stride + 1) * sizeof(int32_t);
 }
 
 rtp_status rtp_paged_evict(const rtp_paged_kv* kv, const int32_t* seq_len, int32_t budget, int32_t n_recent,
@@ -277,6 +282,7 @@ rtp_status rtp_paged_evict(const rtp_paged_kv* kv, const int32_t* seq_len, int32
   a.out_positions = out_positions;
   a.out_len = out_len;
   a.moves = static_cast<int32_t*>(workspace);
+  a.n_moves = a.moves + (size_t)kv->n_seqs * kv->n_kv_heads * stride;
   const cudaError_t e = launch_paged_evict(a, stream);
   return e == cudaSuccess ? RTP_OK : cuda_fail(nullptr, e, fn);
 }

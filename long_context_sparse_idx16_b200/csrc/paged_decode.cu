@@ -25,8 +25,6 @@
 //     two dims of two keys, which a byte permute splits over two output tiles.
 // Accumulated weights need the final log-sum-exp: the scores go through the workspace in fp32 and
 // weights_kernel adds exp(s - lse) over the query heads.
-#include <atomic>
-#include <mutex>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -105,37 +103,6 @@ __device__ __forceinline__ Entry entry_of(const AttnArgs& a, int e) {
 
 // First tile of CTA c's range.
 __device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) { return total * c / ctas; }
-
-// ---- types of the products
-
-template <typename T>
-__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if constexpr (std::is_same_v<T, __half>)
-    mma16816(c, a, b0, b1);
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (std::is_same_v<T, __half>) return pack_half2(x, y);
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// two e4m3 values (low 16 bits) as two T, exactly
-template <typename T>
-__device__ __forceinline__ uint32_t widen2(uint32_t x) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
-  const __half2 y = *reinterpret_cast<const __half2*>(&h);
-  if constexpr (std::is_same_v<T, __half>) return *reinterpret_cast<const uint32_t*>(&y);
-  const float2 f = __half22float2(y);
-  return pack2<T>(f.x, f.y);
-}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
                                             uint32_t mbar) {
@@ -741,34 +708,12 @@ bool map_pages(CUtensorMap* m, void* base, const int64_t* stride, const rtp_page
                     bx, bytes < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Launch that may start while the kernel before it drains; it waits (griddepcontrol.wait) before
-// it reads what that kernel wrote.
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = grid;
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, fn, args...);
-}
-
 template <typename QT, typename K, int D>
 cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int grid, cudaStream_t st) {
   using S = Stage<K, D>;
   constexpr size_t smem = (size_t)S::kStages * 2 * S::kHalf + 1024;
-  static std::once_flag once[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::call_once(once[dev & 63], [&] {
-    e = cudaFuncSetAttribute(attn_kernel<QT, K, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  });
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(attn_kernel<QT, K, D>, smem, done);
   if (e != cudaSuccess) return e;
   if (a.n_entries > kInline) {
     plan_kernel<<<1, 1024, 0, st>>>(a);

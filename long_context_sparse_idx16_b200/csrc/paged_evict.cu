@@ -1,25 +1,59 @@
 // paged_evict.cu -- a cache brought back to a budget by the attention weight its slots drew.
 //
-// Slots are ranked by a 64-bit key, larger first: (score order key << 32) | ~position, the upper
-// half all ones for the slots that always stay (sinks and the newest).  The budget-th largest key
-// is the cut; equal keys take the lower slot.  Survivors behind the budget fill the freed slots
-// below it, both in slot order, so exactly as many rows move as slots below the budget are freed.
+// Slots are ranked by the 32-bit order key of their score, all ones for the slots that always stay
+// (sinks and the newest); the budget-th largest key is the cut, equal keys take the lower position,
+// then the lower slot.  Survivors behind the budget fill the freed slots below it, both in slot
+// order, so exactly as many rows move as slots below the budget are freed, and no row moves that
+// can stay.
+//
+// pick_kernel: one CTA per (sequence, KV head) reads scores and positions, keeps the keys in shared
+// memory (beyond 48K slots it forms them again in each pass), finds the cut in three radix passes
+// and writes the two lists.  move_kernel: the rows, 16 bytes a lane, over the whole GPU; HBM bounds
+// it (each moved row is read and written once).
 #include "paged.cuh"
 
 namespace rtp {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
+constexpr int kBins = 2048;
+constexpr int kKeysInSmem = 48 * 1024;
 
-// One CTA per (KV head, sequence).
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
+struct PickShared {
+  uint32_t hist[kBins];
+  uint32_t small[257];
+  int a[33], b[33];
+  int newest, bin, above, exact;
+};
+
+// Finds the bin of the `want`-th largest key in hist: its number and the keys in the bins above it.
+__device__ void find_bin(PickShared& s, int want) {
+  // thread t holds bins kBins - 1 - 2 t and the one below it
+  const int t = threadIdx.x;
+  const int c0 = (int)s.hist[kBins - 1 - 2 * t], c1 = (int)s.hist[kBins - 2 - 2 * t];
+  int total;
+  const int before = block_exclusive(c0 + c1, s.a, &total);
+  if (before < want && before + c0 >= want) {
+    s.bin = kBins - 1 - 2 * t;
+    s.above = before;
+    s.exact = before + c0 == want;
+  } else if (before + c0 < want && before + c0 + c1 >= want) {
+    s.bin = kBins - 2 - 2 * t;
+    s.above = before + c0;
+    s.exact = before + c0 + c1 == want;
+  }
+  __syncthreads();
+}
+
+template <bool kSmem>
+__global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
+  extern __shared__ uint32_t keys[];
+  __shared__ PickShared s;
   const PagedView& kv = a.kv;
-  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  __shared__ uint32_t hist[257];
-  __shared__ int sums[33];
-  __shared__ int s_newest;
-  const int64_t base = ((int64_t)b * kv.Hkv + g) * a.stride;
+  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t prob = (int64_t)b * kv.Hkv + g, base = prob * a.stride;
   const float* sc = a.scores + base;
   const int32_t* pos = a.positions + base;
   int seq;
@@ -27,92 +61,181 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a) {
   if (g == 0 && tid == 0 && paged_row_bad(kv, nullptr, a.seq_len, b)) paged_err(kv, RTP_PAGED_ERANGE);
   const int keep = min(n, a.budget);
   if (g == 0 && tid == 0) a.out_len[b] = keep;
-  int32_t* mover = a.moves + base;
+  const bool apart = a.out_scores != a.scores || a.out_positions != a.positions;
+  int moved = 0;
   if (keep < n) {
-    if (tid == 0) s_newest = INT32_MIN;
+    if (tid == 0) s.newest = INT32_MIN;
     __syncthreads();
     int newest = INT32_MIN;
+#pragma unroll 4
     for (int i = tid; i < n; i += kThreads) newest = max(newest, pos[i]);
-    for (int o = 16; o > 0; o >>= 1) newest = max(newest, __shfl_xor_sync(0xffffffffu, newest, o));
-    if ((tid & 31) == 0) atomicMax(&s_newest, newest);
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    if (lane == 0) atomicMax(&s.newest, newest);
     __syncthreads();
-    const int64_t recent = (int64_t)s_newest - a.n_recent;
-    auto key = [&](int i) -> unsigned long long {
+    const int64_t recent = (int64_t)s.newest - a.n_recent;
+    const auto form = [&](int i) -> uint32_t {
       const int p = pos[i];
       const float x = sc[i];
-      const uint32_t hi = p < a.n_sink || p > recent ? 0xffffffffu : x != x ? 0u : order_key(x + 0.f);
-      return (unsigned long long)hi << 32 | (uint32_t)~((uint32_t)p ^ 0x80000000u);
+      return p < a.n_sink || p > recent ? 0xffffffffu : x != x ? 0u : order_key(x + 0.f);
     };
-    int ties;
-    const unsigned long long cut = block_kth_largest(n, keep, hist, &ties, key);
-    // movers first, in slot order, then the holes they fill (as many)
-    int tied = 0, moved = 0, total;
+    if (kSmem) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kThreads) keys[i] = form(i);
+    }
+    const auto key = [&](int i) -> uint32_t { return kSmem ? keys[i] : form(i); };
+
+    // the cut: digits of 11, 11 and 10 bits; done early when a bin is taken whole
+    uint32_t cut = 0;
+    int want = keep;
+    bool whole = false;
+#pragma unroll 1
+    for (int d = 0; d < 3 && !whole; ++d) {
+      const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+      for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < n; i += kThreads) {
+        const uint32_t x = key(i);
+        if (d == 0 || (x >> (d == 1 ? 21 : 10)) == (cut >> (d == 1 ? 21 : 10)))
+          atomicAdd(&s.hist[d == 2 ? x & 1023u : (x >> shift) & 2047u], 1u);
+      }
+      __syncthreads();
+      find_bin(s, want);
+      cut |= (uint32_t)s.bin << shift;
+      want -= s.above;
+      whole = s.exact != 0;
+      __syncthreads();
+    }
+    // ties: of the slots whose key is the cut, the `want` of lowest (position, slot)
+    unsigned long long tie_cut = 0;
+    if (!whole) {
+      int ties;
+      tie_cut = block_kth_largest(n, want, s.small, &ties, [&](int i) -> unsigned long long {
+        if (key(i) != cut) return 0ull;
+        return (unsigned long long)~((uint32_t)pos[i] ^ 0x80000000u) << 32 | ~(uint32_t)i;
+      });
+    }
+    const auto stays = [&](int i) -> bool {
+      const uint32_t x = key(i);
+      if (x != cut || whole) return x >= cut;
+      return ((unsigned long long)~((uint32_t)pos[i] ^ 0x80000000u) << 32 | ~(uint32_t)i) >= tie_cut;
+    };
+
+    // the lists: a warp takes a contiguous piece, counts, and writes behind the pieces before it
+    int32_t* mover = a.moves + base;
     int32_t* hole = mover + (n - keep);
-    int holes = 0;
-    for (int i0 = 0; i0 < n; i0 += kThreads) {
-      const int i = i0 + tid;
-      const unsigned long long x = i < n ? key(i) : 0;
-      const bool eq = i < n && x == cut;
-      const int e = block_exclusive(eq, sums, &total);
-      const bool in = i < n && (x > cut || (eq && tied + e < ties));
-      tied += total;
-      const bool mv = in && i >= keep, ho = i < keep && !in;
-      const int om = block_exclusive(mv, sums, &total);
-      if (mv) mover[moved + om] = i;
-      moved += total;
-      const int oh = block_exclusive(ho, sums, &total);
-      if (ho) hole[holes + oh] = i;
-      holes += total;
+    const int per = (n + kThreads - 1) / kThreads * 32;
+    const int i0 = warp * per, i1 = min(n, i0 + per);
+    int nm = 0, nh = 0;
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
+      const bool in = i < i1 && stays(i);
+      nm += __popc(__ballot_sync(0xffffffffu, in && i >= keep));
+      nh += __popc(__ballot_sync(0xffffffffu, i < i1 && !in && i < keep));
     }
-    __syncthreads();
-    // rows: a warp per move
-    for (int m = tid >> 5; m < moved; m += kThreads / 32) {
-      const int from = mover[m], to = hole[m];
-      const int64_t fp = paged_page(kv, b, from >> kv.page_shift), tp = paged_page(kv, b, to >> kv.page_shift);
-      if (fp < 0 || tp < 0) {
-        if ((tid & 31) == 0) paged_err(kv, RTP_PAGED_ERANGE);
-        continue;
-      }
-      const int fo = from & (kv.page_size - 1), to_ = to & (kv.page_size - 1);
-      for (int c = (tid & 31) * 16; c < 2 * a.row_bytes; c += 512) {
-        if (c < a.row_bytes)
-          *(uint4*)(kv.k + tp * kv.kp + g * kv.kh + to_ * kv.ks + c) =
-              *(const uint4*)(kv.k + fp * kv.kp + g * kv.kh + fo * kv.ks + c);
-        else
-          *(uint4*)(kv.v + tp * kv.vp + g * kv.vh + to_ * kv.vs + c - a.row_bytes) =
-              *(const uint4*)(kv.v + fp * kv.vp + g * kv.vh + fo * kv.vs + c - a.row_bytes);
-      }
-    }
-    // scores and positions: what stays, then what moves in (the sources lie at or behind the budget)
-    if (a.out_scores != a.scores || a.out_positions != a.positions) {
-      for (int i = tid; i < keep; i += kThreads) {
+    int holes;
+    // the sums over warps: each warp's lane 0 carries its count
+    int om = block_exclusive(lane == 0 ? nm : 0, s.a, &moved);
+    int oh = block_exclusive(lane == 0 ? nh : 0, s.b, &holes);
+    om = __shfl_sync(0xffffffffu, om, 0);
+    oh = __shfl_sync(0xffffffffu, oh, 0);
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
+      const bool in = i < i1 && stays(i);
+      const bool mv = in && i >= keep, ho = i < i1 && !in && i < keep;
+      const uint32_t bm = __ballot_sync(0xffffffffu, mv), bh = __ballot_sync(0xffffffffu, ho);
+      if (mv) mover[om + __popc(bm & below)] = i;
+      if (ho) hole[oh + __popc(bh & below)] = i;
+      om += __popc(bm);
+      oh += __popc(bh);
+      if (apart && in && i < keep) {
         a.out_scores[base + i] = sc[i];
         a.out_positions[base + i] = pos[i];
       }
-      __syncthreads();
-    }
-    for (int m = tid; m < moved; m += kThreads) {
-      a.out_scores[base + hole[m]] = sc[mover[m]];
-      a.out_positions[base + hole[m]] = pos[mover[m]];
     }
     __syncthreads();
-  } else {
+    // what moves in: the sources lie at or behind the budget, where nothing has been written yet
+    for (int m = tid; m < moved; m += kThreads) {
+      const int to = hole[m], from = mover[m];
+      a.out_scores[base + to] = sc[from];
+      a.out_positions[base + to] = pos[from];
+    }
+    __syncthreads();
+  } else if (apart) {
     for (int i = tid; i < keep; i += kThreads) {
       a.out_scores[base + i] = sc[i];
       a.out_positions[base + i] = pos[i];
     }
   }
-  for (int i = keep + tid; i < a.stride; i += kThreads) {
+  if (tid == 0) a.n_moves[prob] = moved;
+  for (int64_t i = keep + tid; i < a.stride; i += kThreads) {
     a.out_scores[base + i] = 0.f;
     a.out_positions[base + i] = -1;
+  }
+}
+
+// kMoveRows moves of one (sequence, KV head) per CTA: P = 2 row_bytes / 16 lanes per row (K, then V).
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 64;
+
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
+  const PagedView& kv = a.kv;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const int64_t prob = (int64_t)b * kv.Hkv + g, base = prob * a.stride;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int moved = a.n_moves[prob];
+  if ((int64_t)blockIdx.x * kMoveRows >= moved) return;
+  int seq;
+  const int n = paged_row(kv, nullptr, a.seq_len, b, &seq);
+  const int32_t* mover = a.moves + base;
+  const int32_t* hole = mover + (n - min(n, a.budget));
+  __shared__ uint8_t* from_to[2][2][kMoveRows];  // [from, to][K, V]
+  const int m0 = blockIdx.x * kMoveRows, rows = min(kMoveRows, moved - m0);
+  if (threadIdx.x < 2 * rows) {
+    const int m = threadIdx.x >> 1, to = threadIdx.x & 1;
+    const int slot = to ? hole[m0 + m] : mover[m0 + m];
+    const int64_t page = paged_page(kv, b, slot >> kv.page_shift);
+    const int off = slot & (kv.page_size - 1);
+    if (page < 0) paged_err(kv, RTP_PAGED_ERANGE);
+    from_to[to][0][m] = page < 0 ? nullptr : kv.k + page * kv.kp + g * kv.kh + off * kv.ks;
+    from_to[to][1][m] = page < 0 ? nullptr : kv.v + page * kv.vp + g * kv.vh + off * kv.vs;
+  }
+  __syncthreads();
+  const int half = a.row_bytes / 16;  // lanes of a K or V row: 4, 8 or 16
+  const int x = threadIdx.x % half, which = (threadIdx.x / half) & 1, step = kMoveThreads / (2 * half);
+  constexpr int kUnroll = 4;
+  for (int m = threadIdx.x / (2 * half); m < rows; m += step * kUnroll) {
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = m + u * step;
+      if (r < rows && from_to[0][which][r] && from_to[1][which][r]) v[u] = ((const uint4*)from_to[0][which][r])[x];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = m + u * step;
+      if (r < rows && from_to[0][which][r] && from_to[1][which][r]) ((uint4*)from_to[1][which][r])[x] = v[u];
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_evict(const EvictArgs& a, cudaStream_t st) {
-  evict_kernel<<<dim3(a.kv.Hkv, a.kv.n_seqs), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  const int64_t cap = (int64_t)a.kv.max_pages << a.kv.page_shift;
+  const dim3 grid(a.kv.Hkv, a.kv.n_seqs);
+  cudaError_t e;
+  if (cap <= kKeysInSmem) {
+    static std::atomic<uint64_t> done{0};
+    if ((e = allow_smem(pick_kernel<true>, kKeysInSmem * sizeof(uint32_t), done)) != cudaSuccess) return e;
+    pick_kernel<true><<<grid, kThreads, cap * sizeof(uint32_t), st>>>(a);
+  } else {
+    pick_kernel<false><<<grid, kThreads, 0, st>>>(a);
+  }
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // at most the smaller of the slots kept and the slots dropped move
+  const int64_t most = cap - a.budget < a.budget ? cap - a.budget : a.budget;
+  if (most <= 0) return cudaSuccess;
+  return launch_after(move_kernel, dim3((unsigned)((most + kMoveRows - 1) / kMoveRows), a.kv.Hkv, a.kv.n_seqs),
+                      kMoveThreads, 0, st, a);
 }
 
 }  // namespace rtp

@@ -1,105 +1,486 @@
 // paged_select.cu -- the pages a query attends to, by an upper bound of its scores in each page.
 //
-// For KV head g: score(page) = max_h sum_d max(q_hd lo_d, q_hd hi_d) over g's query heads h, in
-// fp64 (products of 16-bit values are exact there and sums of 128 nearly always are, so the order
-// of summation does not move a page across the cut).  The top pages come from a radix select over
-// the order-preserving 64-bit keys of the scores; ties take the lower page.
+// For KV head g: score(page) = max_h sum_d max(q_hd lo_d, q_hd hi_d) over g's query heads h, which is
+// [max(q, 0), min(q, 0)] . [hi, lo]: a product with 2 D terms.  The top pages by the exact (fp64)
+// scores are wanted, ties to the lower page; that takes two steps:
+//   * page_score_kernel forms all scores on the tensor cores (mma.sync, fp32 sums).  Products of
+//     16-bit values are exact, so a score is off by at most eps = 2^-14 |q|_1 max|bound|: 2 D / 16
+//     steps that each add 16 products and the running sum, every term cut at 2^-23 of the largest,
+//     make at most 16 * 17 * 2^-23 < 2^-14.9 of the sum of all magnitudes.
+//   * page_pick_kernel finds the bin of the last page taken in a linear histogram of these scores.
+//     Pages above the bin by 2 eps are in, pages below it by 2 eps are out; the few between get
+//     their exact fp64 scores and are ranked by them.  Where too many are between (equal scores,
+//     infinities, NaN) all of them are scored exactly and a radix select over their 64-bit keys
+//     decides.
+// The bounds are read once per row (once per eight rows of a sequence that follow one another),
+// 4 D bytes a page in 16 bits: HBM bounds the scoring of decode rows, the tensor cores that of chunks.
 #include "paged.cuh"
 
 namespace rtp {
 
 namespace {
 
-constexpr int kThreads = 256;
+// ---- scores
 
-// A warp per page.
-template <typename T, typename K>
-__global__ void __launch_bounds__(kThreads) page_score_kernel(const SelectPagesArgs a) {
+constexpr int kScoreWarps = 8;
+constexpr int kPagesPerWarp = kPageChunk / kScoreWarps;  // 32
+constexpr int kRowBlock = 8;  // rows of a chunk that share one read of the bounds
+constexpr int kMaxM = kRowBlock * 64;  // heads of a run of rows, at most
+
+template <typename T>
+__device__ __forceinline__ uint32_t pos_part(uint32_t x) {
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 y = __hmax2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const __nv_bfloat162 y = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&x), __bfloat162bfloat162(__ushort_as_bfloat16(0)));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t neg_part(uint32_t x) {
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 y = __hmin2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const __nv_bfloat162 y = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&x), __bfloat162bfloat162(__ushort_as_bfloat16(0)));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+// running maximum of magnitudes, in T pairs (NaN shows in the scores themselves)
+template <typename T>
+__device__ __forceinline__ uint32_t abs_max(uint32_t m, uint32_t x) {
+  x &= 0x7fff7fffu;
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 y = __hmax2(*reinterpret_cast<__half2*>(&m), *reinterpret_cast<__half2*>(&x));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const __nv_bfloat162 y = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), *reinterpret_cast<__nv_bfloat162*>(&x));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// A run of rows of one sequence inside a block of kRowBlock rows.
+struct Run {
+  int first, count, seq, pages;  // pages: of its longest row
+};
+__device__ __forceinline__ Run run_at(const SelectPagesArgs& a, int r, int end) {
+  Run u;
+  u.first = r;
+  int len = paged_row(a.kv, a.row_seq, a.row_len, r, &u.seq);
+  u.count = 1;
+  while (r + u.count < end && a.row_seq[r + u.count] == a.row_seq[r]) {
+    int s;
+    len = max(len, paged_row(a.kv, a.row_seq, a.row_len, r + u.count, &s));
+    ++u.count;
+  }
+  u.pages = (int)(((int64_t)len + a.kv.page_size - 1) >> a.kv.page_shift);
+  return u;
+}
+
+// One CTA: a chunk of pages, a KV head, a block of rows.  A warp takes 32 pages, 16 at a time: a lane
+// holds E = 16 bytes' worth of successive dims of page (lane / 4) of an 8-page tile, dims
+// (4 j + lane % 4) E ... of load j, and the query operand is read in the same order, so the
+// contraction needs no shuffling.
+template <typename T, typename K, int D>
+__global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const SelectPagesArgs a, int row_block, int m_pad) {
+  constexpr int E = 16 / (int)sizeof(K);
+  constexpr int J = D / (4 * E);  // loads per bound
+  constexpr int KS = D / 16;      // steps of 16 terms per bound
+  constexpr int QS = D + 32;      // elements between query rows: 64 bytes off, two rows cover all banks
+  extern __shared__ __align__(16) uint8_t smem_[];
+  uint16_t* sq = reinterpret_cast<uint16_t*>(smem_);                                // [m_pad][QS]
+  uint32_t* best = reinterpret_cast<uint32_t*>(smem_ + (size_t)m_pad * QS * 2);     // [row_block][kPageChunk]
+  __shared__ uint32_t s_max;
   const PagedView& kv = a.kv;
-  const int g = blockIdx.y, r = blockIdx.z, lane = threadIdx.x & 31;
-  int b;
-  const int len = paged_row(kv, a.row_seq, a.row_len, r, &b);
-  const int pages = (len + kv.page_size - 1) >> kv.page_shift;
-  const T* q = (const T*)a.q + r * a.q_stride + (int64_t)g * a.group * kv.D;
-  unsigned long long* keys = a.keys + ((int64_t)r * kv.Hkv + g) * kv.max_pages;
-  for (int i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < pages; i += gridDim.x * (kThreads / 32)) {
-    unsigned long long key;
-    const int64_t page = paged_page(kv, b, i);
-    if (i < a.n_first || i >= pages - a.n_recent) {
-      key = ~0ull;
-    } else if (page < 0) {
-      if (lane == 0) paged_err(kv, RTP_PAGED_ERANGE);
-      key = 0;
-    } else {
-      const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * kv.D;
-      double best = -INFINITY;
-      bool nan = false;
-      for (int u = 0; u < a.group; ++u) {
-        double s = 0.0;
-        for (int d = lane; d < kv.D; d += 32) {
-          const double x = to_f32(q[u * kv.D + d]);
-          s += x * to_f32(x < 0.0 ? lim[d] : lim[kv.D + d]);
-        }
-        s = warp_sum(s);
-        nan |= s != s;
-        best = fmax(best, s);
-      }
-      key = nan ? 0ull : order_key64(best);
+  const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r_end = min(a.n_rows, ((int)blockIdx.z + 1) * row_block);
+  asm volatile("griddepcontrol.launch_dependents;");
+  for (int r = blockIdx.z * row_block; r < r_end;) {
+    const Run u = run_at(a, r, r_end);
+    r += u.count;
+    const int p0 = blockIdx.x * kPageChunk;
+    if (p0 >= u.pages) continue;  // the whole CTA alike
+    const int m_rows = u.count * a.group, m_tiles = (m_rows + 15) / 16;
+    __syncthreads();
+    for (int i = tid; i < m_tiles * 16 * (D / 8); i += 32 * kScoreWarps) {
+      const int m = i / (D / 8), x = i % (D / 8);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (m < m_rows)
+        v = *(const uint4*)((const T*)a.q + (u.first + m / a.group) * a.q_stride +
+                            (int64_t)(g * a.group + m % a.group) * D + x * 8);
+      *(uint4*)(sq + m * QS + x * 8) = v;
     }
-    if (lane == 0) keys[i] = key;
+    for (int i = tid; i < u.count * kPageChunk; i += 32 * kScoreWarps) best[i] = 0u;
+    if (tid == 0) s_max = 0u;
+    __syncthreads();
+    uint32_t mag = 0u;
+    for (int n0 = 0; n0 < kPagesPerWarp; n0 += 16) {
+      const int pw = p0 + warp * kPagesPerWarp + n0;
+      if (pw >= u.pages) break;
+      // the bounds of two tiles of 8 pages: B operands [tile][hi, lo][step][2]
+      uint32_t bb[2][2][KS][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int p = pw + t * 8 + (lane >> 2);
+        const int64_t page = p < u.pages ? paged_page(kv, u.seq, p) : -1;
+        const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * D + (lane & 3) * E;
+        if (p < u.pages && page < 0 && (lane & 3) == 0)  // no number: the exact path ranks it last
+          for (int i = 0; i < u.count; ++i) atomicMax(&best[i * kPageChunk + p - p0], 0xffffffffu);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const uint4 v = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : ld_nc_u4(lim + (x ? 0 : D) + j * 4 * E);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (sizeof(K) == 1) {
+                bb[t][x][4 * j + e][0] = widen2<T>(w[e]);
+                bb[t][x][4 * j + e][1] = widen2<T>(w[e] >> 16);
+              } else {
+                bb[t][x][2 * j + (e >> 1)][e & 1] = w[e];
+              }
+            }
+          }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int k = 0; k < KS; ++k) mag = abs_max<T>(abs_max<T>(mag, bb[t][x][k][0]), bb[t][x][k][1]);
+      }
+      for (int mt = 0; mt < m_tiles; ++mt) {
+        float c[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          // terms of step k: dims of this lane (4 of E successive ones)
+          const int dim = sizeof(K) == 1 ? ((k >> 2) * 4 + (lane & 3)) * E + (k & 3) * 4
+                                         : ((k >> 1) * 4 + (lane & 3)) * E + (k & 1) * 4;
+          const uint2 q0 = *(const uint2*)(sq + (mt * 16 + (lane >> 2)) * QS + dim);
+          const uint2 q1 = *(const uint2*)(sq + (mt * 16 + 8 + (lane >> 2)) * QS + dim);
+          const uint32_t ap[4] = {pos_part<T>(q0.x), pos_part<T>(q1.x), pos_part<T>(q0.y), pos_part<T>(q1.y)};
+          const uint32_t an[4] = {neg_part<T>(q0.x), neg_part<T>(q1.x), neg_part<T>(q0.y), neg_part<T>(q1.y)};
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            mma<T>(c[t], ap, bb[t][0][k][0], bb[t][0][k][1]);
+            mma<T>(c[t], an, bb[t][1][k][0], bb[t][1][k][1]);
+          }
+        }
+        // the greatest head of each row: through shared memory, as order keys (NaN above all others);
+        // eight heads of one row are joined in registers first where groups are whole eights
+        const bool eights = (a.group & 7) == 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int m = mt * 16 + (lane >> 2) + (e >> 1) * 8;
+            uint32_t key = m >= m_rows ? 0u : c[t][e] != c[t][e] ? 0xffffffffu : order_key(c[t][e]);
+            if (eights) {
+              key = max(key, __shfl_xor_sync(0xffffffffu, key, 4));
+              key = max(key, __shfl_xor_sync(0xffffffffu, key, 8));
+              key = max(key, __shfl_xor_sync(0xffffffffu, key, 16));
+            }
+            if (m < m_rows && (!eights || lane < 4))
+              atomicMax(&best[m / a.group * kPageChunk + warp * kPagesPerWarp + n0 + t * 8 + (lane & 3) * 2 + (e & 1)], key);
+          }
+      }
+    }
+    // magnitude of the bounds seen
+    {
+      const T* h = reinterpret_cast<const T*>(&mag);
+      const float x = fmaxf(to_f32(h[0]), to_f32(h[1]));
+      const uint32_t y = __reduce_max_sync(0xffffffffu, __float_as_uint(x));  // not negative: bits order alike
+      if (lane == 0) atomicMax(&s_max, y);
+    }
+    __syncthreads();
+    for (int i = tid; i < u.count * kPageChunk; i += 32 * kScoreWarps) {
+      const int row = u.first + i / kPageChunk, p = p0 + i % kPageChunk;
+      if (p < u.pages) {
+        const uint32_t key = best[i];
+        a.approx[((int64_t)row * kv.Hkv + g) * kv.max_pages + p] =
+            key == 0xffffffffu ? __uint_as_float(0x7fc00000u) : key_to_float(key);
+      }
+    }
+    for (int i = tid; i < u.count; i += 32 * kScoreWarps)
+      a.chunk_max[((int64_t)(u.first + i) * kv.Hkv + g) * gridDim.x + blockIdx.x] = __uint_as_float(s_max);
   }
 }
 
-// One CTA per (row, KV head): the threshold, then the pages above it in ascending order.
-__global__ void __launch_bounds__(kThreads) page_pick_kernel(const SelectPagesArgs a) {
-  const PagedView& kv = a.kv;
-  const int g = blockIdx.x, r = blockIdx.y;
-  __shared__ uint32_t hist[257];
-  __shared__ int sums[33];
-  int b;
-  const int len = paged_row(kv, a.row_seq, a.row_len, r, &b);
-  if (g == 0 && threadIdx.x == 0 && paged_row_bad(kv, a.row_seq, a.row_len, r)) paged_err(kv, RTP_PAGED_ERANGE);
-  const int pages = (len + kv.page_size - 1) >> kv.page_shift;
-  const int take = min(a.top, pages);
-  const unsigned long long* keys = a.keys + ((int64_t)r * kv.Hkv + g) * kv.max_pages;
-  int32_t* sel = a.sel + ((int64_t)r * kv.Hkv + g) * a.sel_stride;
-  if (threadIdx.x == 0) a.sel_count[(int64_t)r * kv.Hkv + g] = take;
-  for (int i = take + threadIdx.x; i < a.top; i += kThreads) sel[i] = -1;
-  if (take == 0) return;
-  int ties = 0x7fffffff;
-  unsigned long long cut = 0;
-  if (take < pages) cut = block_kth_largest(pages, take, hist, &ties, [&](int i) { return keys[i]; });
-  int at = 0, tied = 0;
-  for (int i0 = 0; i0 < pages; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    const unsigned long long key = i < pages ? keys[i] : 0;
-    const bool eq = i < pages && key == cut;
-    int total;
-    const int e = block_exclusive(eq, sums, &total);
-    const bool in = i < pages && (key > cut || (eq && tied + e < ties));
-    tied += total;
-    const int o = block_exclusive(in, sums, &total);
-    if (in) sel[at + o] = i;
-    at += total;
+// ---- the choice
+
+constexpr int kBins = 1024;
+constexpr int kMaxBetween = 256;  // pages ranked by their exact scores in shared memory
+constexpr int kPagesInSmem = 48 * 1024;
+
+struct PickShared {
+  uint32_t hist[kBins];
+  uint32_t small[257];
+  float fa[32], fb[32];
+  int sums[33];
+  int bin, above, n_between, n_in;
+  float lo, hi;
+  int idx[kMaxBetween];
+  unsigned long long key[kMaxBetween];
+};
+
+template <int kT>
+__device__ __forceinline__ float block_extreme(float x, bool want_max, float* sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, x, o);
+    x = want_max ? fmaxf(x, y) : fminf(x, y);
   }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = sh[0];
+#pragma unroll
+  for (int w = 1; w < kT / 32; ++w) x = want_max ? fmaxf(x, sh[w]) : fminf(x, sh[w]);
+  return x;
+}
+
+// Exact key of a page, by one warp; 0 (last) for a page outside the pool or a score that is no number.
+template <typename T, typename K>
+__device__ unsigned long long exact_key(const SelectPagesArgs& a, const T* q, int seq, int g, int p) {
+  const PagedView& kv = a.kv;
+  const int lane = threadIdx.x & 31;
+  const int64_t page = paged_page(kv, seq, p);
+  if (page < 0) {
+    if (lane == 0) paged_err(kv, RTP_PAGED_ERANGE);
+    return 0ull;
+  }
+  const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * kv.D;
+  double lo[4], hi[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int d = e * 32 + lane;
+    lo[e] = d < kv.D ? to_f32(lim[d]) : 0.f;
+    hi[e] = d < kv.D ? to_f32(lim[kv.D + d]) : 0.f;
+  }
+  double best = -INFINITY;
+  bool nan = false;
+  for (int u = 0; u < a.group; ++u) {
+    double s = 0.0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = e * 32 + lane;
+      const double x = d < kv.D ? to_f32(q[u * kv.D + d]) : 0.f;
+      s += x * (x < 0.0 ? lo[e] : hi[e]);
+    }
+    s = warp_sum(s);
+    nan |= s != s;
+    best = fmax(best, s);
+  }
+  return nan ? 0ull : order_key64(best);
+}
+
+// One CTA of kT threads per (KV head, row); the scores in shared memory, or in the workspace itself.
+template <typename T, typename K, int kT, bool kSmem>
+__global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, int chunks) {
+  extern __shared__ float list_[];
+  __shared__ PickShared s;
+  const PagedView& kv = a.kv;
+  const int g = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int seq;
+  const int len = paged_row(kv, a.row_seq, a.row_len, r, &seq);
+  if (g == 0 && tid == 0 && paged_row_bad(kv, a.row_seq, a.row_len, r)) paged_err(kv, RTP_PAGED_ERANGE);
+  const int64_t prob = (int64_t)r * kv.Hkv + g;
+  const int pages = (int)(((int64_t)len + kv.page_size - 1) >> kv.page_shift);
+  const int take = min(a.top, pages);
+  const int c0 = min(a.n_first, pages), c1 = max(c0, pages - a.n_recent);  // the pages to choose from
+  const int want = take - (pages - (c1 - c0));
+  int32_t* sel = a.sel + prob * a.sel_stride;
+  if (tid == 0) a.sel_count[prob] = take;
+  for (int i = take + tid; i < a.top; i += kT) sel[i] = -1;
+  float* ws = a.approx + prob * kv.max_pages;
+  float* x = kSmem ? list_ : ws;
+  const T* q = (const T*)a.q + r * a.q_stride + (int64_t)g * a.group * kv.D;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float cut = INFINITY;  // pages above it are in
+  if (want > 0 && want < c1 - c0) {
+    // the scores' range; eps
+    float lo = INFINITY, hi = -INFINITY, mag = 0.f, q1 = 0.f;
+    bool odd = false;
+    for (int i = c0 + tid; i < c1; i += kT) {
+      const float y = ws[i];
+      if (kSmem) x[i] = y;
+      lo = fminf(lo, y);
+      hi = fmaxf(hi, y);
+      odd |= !isfinite(y);
+    }
+    for (int i = tid; i < chunks && i * kPageChunk < pages; i += kT) mag = fmaxf(mag, a.chunk_max[prob * chunks + i]);
+    for (int u = warp; u < a.group; u += kT / 32) {
+      float y = 0.f;
+      for (int d = lane; d < kv.D; d += 32) y += fabsf(to_f32(q[u * kv.D + d]));
+      q1 = fmaxf(q1, warp_sum(y));
+    }
+    lo = block_extreme<kT>(lo, false, s.fa);
+    hi = block_extreme<kT>(hi, true, s.fb);
+    mag = block_extreme<kT>(mag, true, s.fa);
+    q1 = block_extreme<kT>(q1, true, s.fb);
+    // 1.01 covers the rounding of |q|_1 and of this product; 2^-110 what underflows in fp32
+    const float eps = 1.01f * 6.103515625e-05f * q1 * mag + 7.7e-34f;
+    odd = __syncthreads_or(odd || !isfinite(eps));
+    bool done = false;
+    float cut_lo = -INFINITY;
+    for (int round = 0; round < 4 && !odd && !done; ++round) {
+      // histogram of [lo, hi]; the page wanted last lies in it
+      for (int i = tid; i < kBins; i += kT) s.hist[i] = 0;
+      if (tid == 0) s.n_between = s.n_in = 0;
+      __syncthreads();
+      const float scale = hi > lo ? kBins / (hi - lo) : 0.f;
+      const auto bin_of = [&](float y) { return min(kBins - 1, (int)((y - lo) * scale)); };
+      int above = 0;
+      for (int i = c0 + tid; i < c1; i += kT) {
+        const float y = x[i];
+        if (y > hi) ++above;
+        else if (y >= lo) atomicAdd(&s.hist[bin_of(y)], 1u);
+      }
+      above = __reduce_add_sync(0xffffffffu, above);
+      if (lane == 0 && above) atomicAdd(&s.n_in, above);
+      __syncthreads();
+      above = s.n_in;
+      constexpr int B = kBins / kT;
+      int c[B], sum = 0, total;
+#pragma unroll
+      for (int e = 0; e < B; ++e) sum += c[e] = (int)s.hist[kBins - 1 - (tid * B + e)];
+      int before = above + block_exclusive(sum, s.sums, &total);
+#pragma unroll
+      for (int e = 0; e < B; ++e) {
+        if (before < want && before + c[e] >= want) s.bin = kBins - 1 - (tid * B + e);
+        before += c[e];
+      }
+      if (tid == 0) s.n_in = 0;
+      __syncthreads();
+      const int bin = s.bin;
+      // the bin's own range, then everything within 2 eps of it
+      float blo = INFINITY, bhi = -INFINITY;
+      for (int i = c0 + tid; i < c1; i += kT) {
+        const float y = x[i];
+        if (y >= lo && y <= hi && bin_of(y) == bin) {
+          blo = fminf(blo, y);
+          bhi = fmaxf(bhi, y);
+        }
+      }
+      blo = block_extreme<kT>(blo, false, s.fa);
+      bhi = block_extreme<kT>(bhi, true, s.fb);
+      cut = __fadd_ru(bhi, 2.f * eps);
+      cut_lo = __fadd_rd(blo, -2.f * eps);
+      int in = 0;
+      for (int i = c0 + tid; i < c1; i += kT) {
+        const float y = x[i];
+        if (y > cut) {
+          ++in;
+        } else if (y >= cut_lo) {
+          const int at = atomicAdd(&s.n_between, 1);
+          if (at < kMaxBetween) s.idx[at] = i;
+        }
+      }
+      in = __reduce_add_sync(0xffffffffu, in);
+      if (lane == 0 && in) atomicAdd(&s.n_in, in);
+      __syncthreads();
+      done = s.n_between <= kMaxBetween;
+      if (!done && bhi - blo <= 4.f * eps) break;  // a finer histogram would not help
+      lo = blo;
+      hi = bhi;
+      __syncthreads();
+    }
+    if (done) {
+      const int m = s.n_between, need = want - s.n_in;
+      for (int j = warp; j < m; j += kT / 32) {
+        const unsigned long long k = exact_key<T, K>(a, q, seq, g, s.idx[j]);
+        if (lane == 0) s.key[j] = k;
+      }
+      __syncthreads();
+      for (int j = tid; j < m; j += kT) {
+        const unsigned long long k = s.key[j];
+        const int i = s.idx[j];
+        int rank = 0;
+        for (int l = 0; l < m; ++l) rank += s.key[l] > k || (s.key[l] == k && s.idx[l] < i);
+        x[i] = rank < need ? INFINITY : -INFINITY;
+      }
+      if (cut == INFINITY) cut = 3.402823466e+38f;  // an overflowed sum: the chosen still lie above
+      __syncthreads();
+    } else {
+      // every page by its exact score
+      unsigned long long* keys = a.keys + prob * kv.max_pages;
+      for (int i = c0 + warp; i < c1; i += kT / 32) {
+        const unsigned long long k = exact_key<T, K>(a, q, seq, g, i);
+        if (lane == 0) keys[i] = k;
+      }
+      __syncthreads();
+      int ties;
+      const unsigned long long kth = block_kth_largest(c1 - c0, want, s.small, &ties, [&](int i) { return keys[c0 + i]; });
+      int tied = 0;
+      for (int i0 = c0; i0 < c1; i0 += kT) {
+        const int i = i0 + tid;
+        const unsigned long long k = i < c1 ? keys[i] : 0ull;
+        const bool eq = i < c1 && k == kth;
+        int total;
+        const int e = block_exclusive(eq, s.sums, &total);
+        if (i < c1) x[i] = k > kth || (eq && tied + e < ties) ? INFINITY : -INFINITY;
+        tied += total;
+      }
+      cut = 0.f;
+      __syncthreads();
+    }
+  }
+  // the pages taken, ascending: a warp takes a contiguous piece
+  const bool all = want >= c1 - c0;
+  const int per = (pages + kT - 1) / kT * 32;
+  const int i0 = warp * per, i1 = min(pages, i0 + per);
+  const auto taken = [&](int i) { return i < c0 || i >= c1 || all || (want > 0 && x[i] > cut); };
+  int n = 0;
+  for (int i = i0 + lane; i - lane < i1; i += 32) n += __popc(__ballot_sync(0xffffffffu, i < i1 && taken(i)));
+  int total;
+  int at = block_exclusive(lane == 0 ? n : 0, s.sums, &total);
+  at = __shfl_sync(0xffffffffu, at, 0);
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const bool in = i < i1 && taken(i);
+    const uint32_t bits = __ballot_sync(0xffffffffu, in);
+    if (in) sel[at + __popc(bits & ((1u << lane) - 1u))] = i;
+    at += __popc(bits);
+  }
+}
+
+template <typename T, typename K, int kT>
+cudaError_t run_pick(const SelectPagesArgs& a, int chunks, cudaStream_t st) {
+  const dim3 grid(a.kv.Hkv, a.n_rows);
+  if (a.kv.max_pages > kPagesInSmem) return launch_after(page_pick_kernel<T, K, kT, false>, grid, kT, 0, st, a, chunks);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(page_pick_kernel<T, K, kT, true>, kPagesInSmem * sizeof(float), done);
+  if (e != cudaSuccess) return e;
+  return launch_after(page_pick_kernel<T, K, kT, true>, grid, kT, a.kv.max_pages * sizeof(float), st, a, chunks);
+}
+
+template <typename T, typename K, int D>
+cudaError_t run_select(const SelectPagesArgs& a, cudaStream_t st) {
+  const int chunks = page_chunks(a.kv.max_pages);
+  const int row_block = a.row_seq ? kRowBlock : 1;
+  const int m_pad = (row_block * a.group + 15) / 16 * 16;
+  const size_t smem = (size_t)m_pad * (D + 32) * 2 + (size_t)row_block * kPageChunk * sizeof(uint32_t);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(page_score_kernel<T, K, D>,
+                             (size_t)kMaxM * (D + 32) * 2 + kRowBlock * kPageChunk * sizeof(uint32_t), done);
+  if (e != cudaSuccess) return e;
+  page_score_kernel<T, K, D><<<dim3(chunks, a.kv.Hkv, (a.n_rows + row_block - 1) / row_block), 32 * kScoreWarps, smem, st>>>(
+      a, row_block, m_pad);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // long lists want more threads for their passes, short ones more CTAs at once
+  return a.kv.max_pages > 2048 ? run_pick<T, K, 1024>(a, chunks, st) : run_pick<T, K, 256>(a, chunks, st);
 }
 
 template <typename T, typename K>
-void run_select(const SelectPagesArgs& a, cudaStream_t st) {
-  const int per = kThreads / 32 * 8;
-  const int blocks = (a.kv.max_pages + per - 1) / per;
-  page_score_kernel<T, K><<<dim3(blocks < 1024 ? blocks : 1024, a.kv.Hkv, a.n_rows), kThreads, 0, st>>>(a);
-  page_pick_kernel<<<dim3(a.kv.Hkv, a.n_rows), kThreads, 0, st>>>(a);
+cudaError_t run_select_d(const SelectPagesArgs& a, cudaStream_t st) {
+  return a.kv.D == 64 ? run_select<T, K, 64>(a, st) : run_select<T, K, 128>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_select(const SelectPagesArgs& a, int qt, int kvt, cudaStream_t st) {
-  if (qt == RTP_FP16 && kvt == RTP_FP16) run_select<__half, __half>(a, st);
-  else if (qt == RTP_BF16 && kvt == RTP_BF16) run_select<__nv_bfloat16, __nv_bfloat16>(a, st);
-  else if (qt == RTP_FP16) run_select<__half, __nv_fp8_e4m3>(a, st);
-  else run_select<__nv_bfloat16, __nv_fp8_e4m3>(a, st);
-  return cudaGetLastError();
+  if (qt == RTP_FP16 && kvt == RTP_FP16) return run_select_d<__half, __half>(a, st);
+  if (qt == RTP_BF16 && kvt == RTP_BF16) return run_select_d<__nv_bfloat16, __nv_bfloat16>(a, st);
+  if (qt == RTP_FP16) return run_select_d<__half, __nv_fp8_e4m3>(a, st);
+  return run_select_d<__nv_bfloat16, __nv_fp8_e4m3>(a, st);
 }
 
 }  // namespace rtp

@@ -541,3 +541,73 @@ def test_graph_replay_and_streams():
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for pair in outs for o in pair)
     assert DT and TINY
+
+
+def test_select_bad_pages_rank_last():
+    from long_context_sparse_idx16_b200 import RTPError
+
+    c = Case([1600], hq=4, hkv=2, d=64, page=16, kv="fp16", seed=3)
+    bounds = torch.from_numpy(stored_bounds(c)).float().to(c.kt).to(c.device)
+    x = c.randn(1, 4, 64).to(c.qt).to(c.device)
+    good = c.table.clone()
+    c.table[0, 7], c.table[0, 60] = 1 << 20, -1
+    cache = c.cache(bounds=bounds)
+    sel, cnt = cache.select_pages(x, c.ints([1600]), 97, n_first=0, n_recent=0)
+    with pytest.raises(RTPError):
+        cache.check()
+    c.table = good
+    for g in range(2):
+        b = f64(bounds)
+        b[[int(good[0, 7]), int(good[0, 60])]] = -np.inf
+        got = sel[0, g].tolist()
+        assert cnt[0, g] == 97 and len(set(got)) == 97 and not {7, 60} & set(got)
+
+
+@pytest.mark.parametrize("n", [5000, 60000 * 16])
+def test_select_long_lists(n):
+    """More pages than one pass of threads; more than shared memory holds (60000 pages of 16)."""
+    c = Case([1], hq=4, hkv=1, d=64, page=16, kv="bf16", seed=3)
+    pages = -(-n // 16)
+    c.table = torch.arange(pages, dtype=torch.int32).flip(0)[None]
+    c.k = torch.zeros((pages, 1, 16, 64), dtype=c.kt, device=c.device)
+    c.v = c.k
+    g = torch.Generator(device="cuda").manual_seed(1)
+    lim = torch.randn((pages, 1, 2, 64), generator=g, device=c.device).abs()
+    lim[:, :, 0] *= -1
+    bounds = lim.to(c.kt)
+    x = c.randn(1, 4, 64).to(c.qt).to(c.device)
+    sel, cnt = c.cache(bounds=bounds).select_pages(x, c.ints([n]), 100, n_first=1, n_recent=2)
+    b = bounds[c.table[0].long().to(c.device), 0].double()
+    q = x[0].double()
+    score = torch.maximum(q[:, None] * b[None, :, 0], q[:, None] * b[None, :, 1]).sum(-1).amax(0)
+    score[0] = score[pages - 2:] = math.inf
+    want = score.sort(descending=True, stable=True).indices[:100].sort().values
+    assert torch.equal(sel[0, 0].long(), want) and int(cnt) == 100
+    # equal scores everywhere: the lowest pages
+    bounds.fill_(0.5)
+    sel, _ = c.cache(bounds=bounds).select_pages(x, c.ints([n]), 50, n_first=0, n_recent=1)
+    assert sel.flatten().tolist() == list(range(49)) + [pages - 1]
+
+
+def test_select_close_scores():
+    """Scores nearer to one another than fp32 sums can tell: the exact order decides."""
+    c = Case([16 * 500], hq=2, hkv=1, d=128, page=16, kv="fp16", seed=3)
+    r = np.random.default_rng(2)
+    base = np.abs(r.standard_normal(128)).astype(np.float16).astype(np.float64) * 30
+    b = np.zeros((c.pool, 1, 2, 128))
+    for p in range(500):
+        # pages differ in one small term only, far below the size of the others
+        t = base.copy()
+        t[p % 128] = 0.0
+        t[127 - p % 128] += 0.0
+        b[int(c.table[0, p]), 0, 1] = base
+        b[int(c.table[0, p]), 0, 1, 0] = 2.0**-14 * (1 + int(r.integers(0, 200)) / 1024)
+    bounds = torch.from_numpy(b).to(c.kt).to(c.device)
+    x = torch.ones((1, 2, 128), dtype=c.qt, device=c.device)
+    sel, _ = c.cache(bounds=bounds).select_pages(x, c.ints([8000]), 40, n_first=0, n_recent=0)
+    assert sel.flatten().tolist() == page_choice(c, f64(bounds), f64(x)[0], 0, 8000, 0, 40, 0, 0)
+
+
+def test_evict_beyond_shared_memory():
+    c = Case([50000, 70], hq=1, hkv=1, d=64, page=16, kv="e4m3", seed=1)
+    run_evict(c, 20000, 100, 4, 3, ties=True)
