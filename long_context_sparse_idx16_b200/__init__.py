@@ -495,4 +495,9 @@ class Layer:
         return {"centres": cent, "counts": counts, "assign": asg, "ready": bool(v.ready)}
 
 
-from .paged import PagedKV  # noqa: E402,F401  (needs the definitions above)
+def __getattr__(name: str):
+    if name == "PagedKV":  # loads torch, which building and the C names do without
+        from .paged import PagedKV
+
+        return PagedKV
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

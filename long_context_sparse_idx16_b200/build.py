@@ -1,4 +1,5 @@
-"""Build librtp.so (the CUDA library behind include/rtp.h) in-tree for sm_100a."""
+"""Build librtp.so (the CUDA library behind include/rtp.h and rtp_paged.h) in-tree for sm_100a, and
+_paged.so, the torch binding of the paged-cache operators."""
 import glob
 import os
 import subprocess
@@ -9,6 +10,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librtp.so")
+EXT = os.path.join(PKG, "_paged.so")
+EXT_SOURCE = os.path.join(CSRC, "paged_torch.cpp")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -33,11 +37,35 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_binding(force: bool = False) -> str:
+    """The torch binding: links to librtp.so beside it and to torch."""
+    deps = [EXT_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(EXT) and all(os.path.getmtime(d) <= os.path.getmtime(EXT) for d in deps):
+        return EXT
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ce
+
+    cmd = [CXX, "-shared", "-fPIC", "-O2", "-std=c++17", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-DTORCH_EXTENSION_NAME=_paged", "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"]]
+    for d in ce.include_paths("cuda"):
+        cmd += ["-isystem", d]
+    cmd += ["-o", EXT, EXT_SOURCE, "-L", PKG, "-l:librtp.so", "-Wl,-rpath,$ORIGIN"]
+    for d in ce.library_paths("cuda"):
+        cmd += ["-L", d]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    subprocess.check_call(cmd)
+    return EXT
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
+        build_binding()
         return LIB
     cmd = [NVCC] + FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-o", LIB] + sources()
     subprocess.check_call(cmd)
+    build_binding(force)
     return LIB
 
 
