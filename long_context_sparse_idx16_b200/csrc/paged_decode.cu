@@ -5,24 +5,29 @@
 //
 // A row reads 2 D elements of cache per key and KV head and does 4 D G flops with them (G query
 // heads per KV head, at most 16 in one pass), so HBM bounds it; the split follows from that:
-//   * The keys of all problems (row, KV head, block of 16 query heads) are cut into tiles of 64
-//     and numbered through.  CTA c of a grid of two per SM takes tiles [c T / G, (c + 1) T / G), so
-//     every SM streams the same bytes whatever the lengths are, and the host need not know them.
-//     A problem that crosses CTAs leaves partial results (running max, sum, unnormalised output),
-//     at most two per CTA, which join_kernel adds up in CTA order.
+//   * The keys of all problems (row, KV head, block of 8 or 16 query heads) are cut into tiles of 64
+//     and numbered through, each problem counting kOverhead tiles more than it has (what starting
+//     and ending it costs).  CTA c of a grid of two or three per SM takes the numbers [c T / G, (c + 1)
+//     T / G), so every SM has the same work whatever the lengths are, and the host need not know
+//     them.  A problem that crosses CTAs leaves partial results (running max, sum, unnormalised
+//     output), at most two per CTA, which join_kernel adds up in CTA order.
 //   * One warp of a CTA feeds a ring of shared-memory stages with TMA boxes of one page each (the
 //     page table is looked up by the lane that issues the box), with the swizzle that ldmatrix
-//     reads without bank conflicts.  Boxes without a slot to attend are not loaded.
+//     reads without bank conflicts.  Boxes without a slot to attend are not loaded.  It also sends
+//     the next problem's queries ahead, so that nobody waits for a problem to begin.
 //   * Four warps take 16 of the 64 keys each, with running maxima and sums of their own, so the
 //     stream needs no barrier between them; their states meet when the problem (or the CTA's part
-//     of it) ends.  The products run on mma.sync: with at most 16 rows a tcgen05 tile (64 or 128
-//     rows) would be mostly padding, and the tensor pipe is not the bound.
+//     of it) ends.  The products run on mma.sync, keys (then dims) as the 16 rows and eight query
+//     heads as the columns: S^T = K Q^T, O^T = V^T P^T, the weights transposed by movmatrix.  A
+//     tcgen05 tile (64 or 128 rows) would be mostly padding, and the tensor pipe is not the bound.
 //   * Scores, maxima, sums and outputs are fp32.  The weights are rounded once to 16 bits for the
 //     product with the values; in fp16 they carry a factor 2^15, so that weights down to 2^-29 of
 //     the largest keep all their bits and sums of many small ones are not lost.
-//   * e4m3 pages are read as 16-bit pairs: ldmatrix gives a lane four successive dims of a key,
-//     which the query fragments match by the same permutation of the contraction, and (transposed)
-//     two dims of two keys, which a byte permute splits over two output tiles.
+//   * e4m3 pages are read as 16-bit pairs and widened to fp16 (exactly): ldmatrix gives a lane four
+//     successive dims of a key, which the query fragments match by the same permutation of the
+//     contraction, and (transposed) two dims of two keys, which a byte permute splits over two
+//     output rows.  Their queries are scaled per head by a power of two into fp16's range, which is
+//     exact for values down to 2^-29 of the head's largest and off by 2^-40 of that below.
 // Accumulated weights need the final log-sum-exp: the scores go through the workspace in fp32 and
 // weights_kernel adds exp(s - lse) over the query heads.
 #include <type_traits>
@@ -37,35 +42,28 @@ namespace {
 constexpr int kTile = 64;         // keys per stage
 constexpr int kConsumers = 4;     // warps, 16 keys of a tile each
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kHeads = 16;        // query heads of a problem
-constexpr int kPerSm = 2;         // CTAs per SM
-constexpr int kRingBytes = 96 * 1024;
 constexpr int kInline = 256;      // entries whose tile prefix every CTA forms by itself
-constexpr int kPad = 36;          // floats per row of the exchange buffer (32 used)
 constexpr int kNoSlot = 0x7fff8000;  // beyond every length: a box none of whose slots is attended
+constexpr int kOverhead = 2;      // tiles' worth of time that a problem costs besides its tiles
+constexpr int kMaxPerSm = 3;
 
-constexpr int stages_of(int stage_bytes) { return kRingBytes / stage_bytes > 8 ? 8 : kRingBytes / stage_bytes; }
-
-struct Shared {
-  unsigned long long full[8], empty[8];
-  int base[8][4];                      // first slot of each box of a stage
-  float m[kConsumers][kHeads], l[kConsumers][kHeads];
-  int stop;                            // a wait gave up: no more copies
-  int64_t prefix[kInline + 1];
-  float x[kConsumers][kHeads][kPad];
-};
+// Eight query heads need half the registers of sixteen: three CTAs per SM instead of two, with
+// rings of 64 KB instead of 96 KB.
+constexpr int per_sm(int octets) { return octets == 1 ? 3 : 2; }
+constexpr int ring_bytes(int octets) { return octets == 1 ? 64 * 1024 : 96 * 1024; }
 
 struct AttnArgs {
   DecodeArgs d;
-  int blocks;            // blocks of 16 query heads per KV head
+  int octets;            // 8 * octets query heads per problem: 1 or 2
+  int blocks;            // problems per KV head
   int box;               // slots per TMA box: min(page_size, 64)
   int n_entries, mult;   // dense: rows, Hkv * blocks; page lists: rows * Hkv, blocks
-  int64_t* prefix;       // [n_entries + 1] tiles of the entries before (one problem each)
+  int64_t* prefix;       // [n_entries + 1] tiles (with overhead) of the entries before, one problem each
   float* lse2;           // [rows][Hq] base-2 log-sum-exp, or NULL
   float* logits;         // [rows][Hq][cap] base-2 scores, or NULL
   int64_t cap;
-  float2* part_ml;       // [2 CTAs][16]
-  float* part_o;         // [2 CTAs][16][D]
+  float2* part_ml;       // [CTAs][continued, begun][16]
+  float* part_o;         // [CTAs][continued, begun][16][D]
 };
 
 // What an entry (a row, or a row's KV head with a page list) attends to.
@@ -101,7 +99,10 @@ __device__ __forceinline__ Entry entry_of(const AttnArgs& a, int e) {
   return n;
 }
 
-// First tile of CTA c's range.
+// Length of an entry's problem in the numbering: its tiles and the overhead.
+__device__ __forceinline__ int64_t units_of(const Entry& n) { return n.tiles ? n.tiles + kOverhead : 0; }
+
+// First number of CTA c's range.
 __device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) { return total * c / ctas; }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
@@ -126,7 +127,9 @@ struct Stage {
   static constexpr int kRow = kBytes < 128 ? kBytes : 128;    // of it per block
   static constexpr int kBlocks = kBytes / kRow;
   static constexpr int kHalf = kTile * kBytes;                // K, and V
-  static constexpr int kStages = stages_of(2 * kHalf);
+  static constexpr int stages(int octets) {
+    return ring_bytes(octets) / (2 * kHalf) > 8 ? 8 : ring_bytes(octets) / (2 * kHalf);
+  }
   // byte offset of 16-byte chunk ch of row r
   static __device__ __forceinline__ uint32_t at(int r, int ch) {
     if constexpr (kRow == 128)
@@ -141,7 +144,7 @@ __device__ __forceinline__ void tile_prefix(const AttnArgs& a, int64_t* out, int
   int64_t run = 0;
   for (int e0 = 0; e0 < a.n_entries; e0 += 32) {
     const int e = e0 + lane;
-    const int64_t t = e < a.n_entries ? entry_of(a, e).tiles : 0;
+    const int64_t t = e < a.n_entries ? units_of(entry_of(a, e)) : 0;
     int64_t y = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnArgs a) {
   int64_t run = 0;
   for (int e0 = 0; e0 < a.n_entries; e0 += 1024) {
     const int e = e0 + tid;
-    const int64_t t = e < a.n_entries ? entry_of(a, e).tiles : 0;
+    const int64_t t = e < a.n_entries ? units_of(entry_of(a, e)) : 0;
     int64_t y = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -185,8 +188,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnArgs a) {
 // Part of the CTA's range inside one problem.
 struct Segment {
   Entry n;
-  int e, prob, first, count;  // entry, its problem, first tile of the problem, tiles
-  bool whole;                 // the problem lies in this CTA alone
+  int e, prob, first, count;  // entry, its problem, first tile of the problem, tiles (perhaps none)
+  int64_t units;              // of the CTA's range
 };
 
 __device__ __forceinline__ Segment segment_at(const AttnArgs& a, const int64_t* prefix, int64_t t, int64_t t1) {
@@ -199,37 +202,80 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& a, const int64_t* 
   }
   s.e = lo;
   s.n = entry_of(a, lo);
-  const int64_t x = t - prefix[lo] * a.mult;
-  s.prob = (int)(x / s.n.tiles);
-  s.first = (int)(x - (int64_t)s.prob * s.n.tiles);
-  s.count = (int)min((int64_t)(s.n.tiles - s.first), t1 - t);
-  s.whole = s.count == s.n.tiles;
+  const int64_t x = t - prefix[lo] * a.mult, u = units_of(s.n);
+  s.prob = (int)(x / u);
+  const int64_t at = x - s.prob * u;
+  s.units = min(u - at, t1 - t);
+  // the overhead comes first
+  s.first = (int)max(at - kOverhead, (int64_t)0);
+  s.count = (int)max(at + s.units - kOverhead - s.first, (int64_t)0);
   return s;
 }
 
-template <typename QT, typename K, int D>
-__global__ void __launch_bounds__(kThreads, kPerSm) attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap km,
-                                                                const __grid_constant__ CUtensorMap vm) {
+// What the consumers need of a segment.
+struct Job {
+  int row, len, lo, sinks;
+  int g, h0, nh;      // KV head, first query head of the group, query heads
+  int first, count;
+  bool whole, last;   // the problem lies in this CTA alone; nothing follows
+};
+
+template <int NB, int D>
+struct Shared {
+  static constexpr int H = 8 * NB;       // query heads
+  static constexpr int R = 32;           // dims of the output exchanged at a time
+  static constexpr int kQRow = 2 * D + 16;  // bytes: rows shifted by 16 bytes, ldmatrix without conflicts
+  uint8_t q[H][kQRow];
+  float x[kConsumers][H][R + 4];
+  float m[kConsumers][H], l[kConsumers][H];
+  unsigned long long full[8], empty[8], job_full, job_empty, meet;
+  int base[8][4];                        // first slot of each box of a stage
+  int stop;                              // a wait gave up
+  Job job;
+  int64_t prefix[kInline + 1];
+};
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(mbar)
+               : "memory");
+}
+
+template <typename QT, typename K, int D, int NB>
+__global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap km,
+                                                                    const __grid_constant__ CUtensorMap vm) {
   using S = Stage<K, D>;
-  using PT = std::conditional_t<std::is_same_v<K, __nv_bfloat16>, __nv_bfloat16, __half>;  // weights, values
+  using Sh = Shared<NB, D>;
   constexpr bool k8 = sizeof(K) == 1;
-  constexpr float kBias = std::is_same_v<PT, __half> ? 15.f : 0.f;
-  constexpr int NT = D / 8;   // output tiles of 8 dims
-  constexpr int KS = D / 16;  // contraction steps of the scores
-  extern __shared__ __align__(1024) uint8_t ring_[];
-  __shared__ Shared sh;
+  using MT = std::conditional_t<k8, __half, K>;  // operands of the products
+  constexpr float kBias = std::is_same_v<MT, __half> ? 15.f : 0.f;
+  constexpr int ST = S::stages(NB);
+  constexpr int KS = D / 16;  // contraction steps of the scores; row tiles of the output
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Sh& sh = *reinterpret_cast<Sh*>(smem + ST * 2 * S::kHalf);
   const DecodeArgs& d = a.d;
   const PagedView& kv = d.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t ring = (smem_u32(ring_) + 1023u) & ~1023u;
+  const uint32_t ring = smem_u32(smem);
   const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty);
+  const uint32_t job_full = smem_u32(&sh.job_full), job_empty = smem_u32(&sh.job_empty), meet = smem_u32(&sh.meet);
+  volatile int* stop = &sh.stop;
   const bool inl = a.n_entries <= kInline;
   if (warp == kConsumers) {
     if (lane == 0) {
-      for (int i = 0; i < S::kStages; ++i) {
+      for (int i = 0; i < ST; ++i) {
         mbar_init(full + 8 * i, 1);
         mbar_init(empty + 8 * i, kConsumers);
       }
+      mbar_init(job_full, 1);
+      mbar_init(job_empty, kConsumers);
+      mbar_init(meet, kConsumers);
       fence_mbar_init();
       sh.stop = 0;
     }
@@ -257,13 +303,39 @@ __global__ void __launch_bounds__(kThreads, kPerSm) attn_kernel(const AttnArgs a
     const int subs = kv.page_size / a.box;
     bool dead = false;
     int st = 0;
-    uint32_t phase = 0;
-    int64_t t = t0;
-    while (t < t1) {
+    uint32_t phase = 0, jphase = 0;
+    for (int64_t t = t0; t < t1 && !dead;) {
       const Segment s = segment_at(a, prefix, t, t1);
+      t += s.units;
+      if (s.count == 0 && t < t1) continue;
       const int g = d.sel ? s.e % kv.Hkv : s.prob / a.blocks;
+      const int h0 = (d.sel ? s.prob : s.prob % a.blocks) * Sh::H;
+      const int nh = min(Sh::H, d.group - h0);
+      dead = !mbar_wait(job_empty, jphase ^ 1u) || *stop;
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) break;
+      if (lane == 0) {
+        Job& j = sh.job;
+        j.row = s.n.row;
+        j.len = s.n.len;
+        j.lo = s.n.lo;
+        j.sinks = s.n.sinks;
+        j.g = g;
+        j.h0 = h0;
+        j.nh = nh;
+        j.first = s.first;
+        j.count = s.count;
+        j.whole = s.count == s.n.tiles;
+        j.last = t >= t1;
+        mbar_expect_tx(job_full, s.count ? nh * 2 * D : 0);
+      }
+      __syncwarp();
+      if (lane < nh && s.count)
+        bulk_load(smem_u32(sh.q[lane]),
+                  (const uint16_t*)d.q + s.n.row * d.q_stride + (int64_t)(g * d.group + h0 + lane) * D, 2 * D, job_full);
+      jphase ^= 1u;
       for (int i = s.first; i < s.first + s.count; ++i) {
-        int base = kNoSlot, page = 0;
+        int base = kNoSlot, page = 0;  // the box's first slot
         if (mine) {
           if (d.sel) {
             const int64_t b = (int64_t)i * boxes + bi;
@@ -286,176 +358,226 @@ __global__ void __launch_bounds__(kThreads, kPerSm) attn_kernel(const AttnArgs a
           }
         }
         const bool load = base != kNoSlot;
-        if (!dead && !mbar_wait(empty + 8 * st, phase ^ 1u)) {
-          dead = true;
-          paged_err(kv, RTP_PAGED_ETIMEOUT);
-        }
-        dead = __any_sync(0xffffffffu, dead || *(volatile int*)&sh.stop != 0);
+        dead = !mbar_wait(empty + 8 * st, phase ^ 1u) || *stop;
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
         const int n_load = __popc(__ballot_sync(0xffffffffu, load));
         if (lane < boxes) sh.base[st][lane] = base;
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(full + 8 * st, dead ? 0u : (uint32_t)(n_load * a.box * S::kRow));
+        if (lane == 0) mbar_expect_tx(full + 8 * st, (uint32_t)(n_load * a.box * S::kRow));
         __syncwarp();
-        if (load && !dead)
+        if (load)
           tma_load_4d(dst0 + st * 2 * S::kHalf, map, blk * (128 / (int)sizeof(K)), base & (kv.page_size - 1), g, page,
                       full + 8 * st);
-        if (++st == S::kStages) {
+        if (++st == ST) {
           st = 0;
           phase ^= 1u;
         }
       }
-      t += s.count;
     }
-    // the consumers have waited for every copy, unless a wait gave up
-    if (dead && lane < S::kStages) mbar_wait(full + 8 * lane, lane < st ? phase : phase ^ 1u);
+    if (dead) {  // the consumers may have left: wait (to a limit) for the copies still in flight
+      if (lane == 0) paged_err(kv, RTP_PAGED_ETIMEOUT);
+      *stop = 1;
+      if (lane < ST) mbar_wait(full + 8 * lane, lane < st ? phase : phase ^ 1u);
+      if (lane == ST) mbar_wait(job_full, jphase ^ 1u);
+    }
     return;
   }
 
   // ---- consumers
   const int r0 = warp * 16, row = lane >> 2, c2 = (lane & 3) * 2;
-  bool dead = false;
+  // a warp that gives up a wait sets `stop` and leaves; the others then run out of their own waits
+  const auto gave_up = [&]() {
+    *stop = 1;
+    if (lane == 0) paged_err(kv, RTP_PAGED_ETIMEOUT);
+  };
   int st = 0;
-  uint32_t phase = 0;
-  int64_t t = t0;
-  while (t < t1) {
-    const Segment s = segment_at(a, prefix, t, t1);
-    const int g = d.sel ? s.e % kv.Hkv : s.prob / a.blocks;
-    const int h0 = (d.sel ? s.prob : s.prob % a.blocks) * kHeads;  // first head of the group
-    const int nh = min(kHeads, d.group - h0);
-    // query fragments (A operands): rows are heads; for e4m3 the contraction slots of a step are
+  uint32_t phase = 0, jphase = 0, mphase = 0;
+  const auto all_meet = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meet);
+    const bool ok = mbar_wait(meet, mphase);
+    mphase ^= 1u;
+    return ok;
+  };
+  for (bool last = false; !last;) {
+    if (!mbar_wait(job_full, jphase)) return gave_up();
+    jphase ^= 1u;
+    const Job j = sh.job;
+    last = j.last;
+    if (j.count == 0) return;  // only ever the last
+    // query fragments (B operands): columns are heads; for e4m3 the contraction slots of a step are
     // permuted as ldmatrix delivers the keys' bytes
-    uint32_t q[KS][4];
-    {
-      const uint16_t* qp = (const uint16_t*)d.q + s.n.row * d.q_stride + (int64_t)(g * d.group + h0) * D;
+    uint32_t q[NB][KS][2];
+    float scale[NB][2];  // of this lane's score columns, heads c2 and c2 + 1 of each octet
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+    for (int n = 0; n < NB; ++n) {
+      if constexpr (!k8) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int h = row + (e & 1) * 8;
-          const int dim = ks * 16 + (k8 ? 2 * c2 + (e >> 1) * 2 : c2 + (e >> 1) * 8);
-          q[ks][e] = h < nh ? *(const uint32_t*)(qp + h * D + dim) : 0u;
+        for (int ks = 0; ks < KS; ks += 2)
+          ldsm_x4(smem_u32(sh.q[n * 8 + (lane & 7)]) + (ks * 2 + (lane >> 3)) * 16, q[n][ks][0], q[n][ks][1],
+                  q[n][ks + 1][0], q[n][ks + 1][1]);
+        scale[n][0] = scale[n][1] = d.scale_log2;
+      } else {
+        // head `row` of the octet: dims 16 ks + 2 c2 ... + 3; scaled by a power of two so that the
+        // largest lies in [2^14, 2^15)
+        const uint8_t* qp = sh.q[n * 8 + row];
+        float top = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint2 u = *(const uint2*)(qp + (ks * 16 + 2 * c2) * 2);
+          const QT* h = reinterpret_cast<const QT*>(&u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(to_f32(h[e])));
         }
-    }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[NT][4];
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = (int)(__float_as_uint(top) >> 23);  // biased exponent
+        // 2^(14 - e) and its inverse, both normal numbers; 1 for zeros, infinities and the like
+        const bool odd = ex < 15 || ex > 253;
+        const float up = odd ? 1.f : __uint_as_float((uint32_t)min(254 + 14 - ex, 253) << 23);
+        const float down = odd ? 1.f : __uint_as_float((uint32_t)max(ex - 14, 1) << 23);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    float* logit = nullptr;
-    if (a.logits) logit = a.logits + ((int64_t)s.n.row * d.Hq + g * d.group + h0) * a.cap;
-
-    for (int i = 0; i < s.count; ++i) {
-      if (!dead && !mbar_wait(full + 8 * st, phase)) {
-        dead = true;
-        *(volatile int*)&sh.stop = 1;
-        if (lane == 0) paged_err(kv, RTP_PAGED_ETIMEOUT);
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint2 u = *(const uint2*)(qp + (ks * 16 + 2 * c2) * 2);
+          const QT* h = reinterpret_cast<const QT*>(&u);
+          q[n][ks][0] = pack2<__half>(to_f32(h[0]) * up, to_f32(h[1]) * up);
+          q[n][ks][1] = pack2<__half>(to_f32(h[2]) * up, to_f32(h[3]) * up);
+        }
+        // lane 4 h holds head h's factor; the score columns are heads c2 and c2 + 1
+        scale[n][0] = d.scale_log2 * __shfl_sync(0xffffffffu, down, c2 * 4);
+        scale[n][1] = d.scale_log2 * __shfl_sync(0xffffffffu, down, c2 * 4 + 4);
       }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(job_empty);
+    float m[NB][2], l[NB][2];
+    float o[NB][KS][4];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
+    }
+    float* logit = nullptr;
+    if (a.logits) logit = a.logits + ((int64_t)j.row * d.Hq + j.g * d.group + j.h0) * a.cap;
+
+    for (int i = 0; i < j.count; ++i) {
+      if (!mbar_wait(full + 8 * st, phase)) return gave_up();
       const int base = sh.base[st][r0 / a.box] + (r0 & (a.box - 1));
-      const bool any = base < s.n.len && (base + 16 > s.n.lo || base < s.n.sinks) && !dead;
-      if (any) {
+      if (base < j.len && (base + 16 > j.lo || base < j.sinks)) {
         const uint32_t kb = ring + st * 2 * S::kHalf, vb = kb + S::kHalf;
-        float z[2][4] = {};
+        float z[NB][4] = {};
         if constexpr (!k8) {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            uint32_t b[4];
-            ldsm_x4(kb + S::at(r0 + (lane >> 4) * 8 + (lane & 7), 2 * ks + ((lane >> 3) & 1)), b[0], b[1], b[2], b[3]);
-            mma<QT>(z[0], q[ks], b[0], b[1]);
-            mma<QT>(z[1], q[ks], b[2], b[3]);
+            uint32_t f[4];
+            ldsm_x4(kb + S::at(r0 + (lane & 15), 2 * ks + (lane >> 4)), f[0], f[1], f[2], f[3]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma<MT>(z[n], f, q[n][ks][0], q[n][ks][1]);
           }
         } else {
 #pragma unroll
           for (int ks = 0; ks < KS; ks += 2) {
             uint32_t b[4];
-            ldsm_x4(kb + S::at(r0 + ((lane >> 3) & 1) * 8 + (lane & 7), ks + (lane >> 4)), b[0], b[1], b[2], b[3]);
+            ldsm_x4(kb + S::at(r0 + (lane & 15), ks + (lane >> 4)), b[0], b[1], b[2], b[3]);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              mma<QT>(z[0], q[ks + u], widen2<QT>(b[2 * u]), widen2<QT>(b[2 * u] >> 16));
-              mma<QT>(z[1], q[ks + u], widen2<QT>(b[2 * u + 1]), widen2<QT>(b[2 * u + 1] >> 16));
+              const uint32_t f[4] = {widen2<MT>(b[2 * u]), widen2<MT>(b[2 * u + 1]), widen2<MT>(b[2 * u] >> 16),
+                                     widen2<MT>(b[2 * u + 1] >> 16)};
+#pragma unroll
+              for (int n = 0; n < NB; ++n) mma<MT>(z[n], f, q[n][ks + u][0], q[n][ks + u][1]);
             }
           }
         }
+        // z: keys base + row (first two) and base + row + 8, heads c2 and c2 + 1
 #pragma unroll
-        for (int u = 0; u < 8; ++u) z[u >> 2][u & 3] *= d.scale_log2;
-        // slots of this lane: base + c2 + {0, 1, 8, 9}
-        const bool part = base + 15 >= s.n.len || !(base >= s.n.lo || base + 15 < s.n.sinks);
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[n][e] *= scale[n][e & 1];
+        const bool part = base + 15 >= j.len || !(base >= j.lo || base + 15 < j.sinks);
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;  // of the values of slots base + c2 + {0, 1, 8, 9}
+        bool ok0 = true, ok1 = true;                        // of this lane's two keys
         if (part) {
-          bool ok[4];
+          const auto ok = [&](int x) { return x < j.len && (x >= j.lo || x < j.sinks); };
+          ok0 = ok(base + row);
+          ok1 = ok(base + row + 8);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int j = base + c2 + (u & 1) + (u >> 1) * 8;
-            ok[u] = j < s.n.len && (j >= s.n.lo || j < s.n.sinks);
-            if (!ok[u]) z[u >> 1][u & 1] = z[u >> 1][2 + (u & 1)] = -INFINITY;
+          for (int n = 0; n < NB; ++n) {
+            if (!ok0) z[n][0] = z[n][1] = -INFINITY;
+            if (!ok1) z[n][2] = z[n][3] = -INFINITY;
           }
-          keep0 = (ok[0] ? 0xffffu : 0u) | (ok[1] ? 0xffff0000u : 0u);
-          keep1 = (ok[2] ? 0xffffu : 0u) | (ok[3] ? 0xffff0000u : 0u);
+          keep0 = (ok(base + c2) ? 0xffffu : 0u) | (ok(base + c2 + 1) ? 0xffff0000u : 0u);
+          keep1 = (ok(base + c2 + 8) ? 0xffffu : 0u) | (ok(base + c2 + 9) ? 0xffff0000u : 0u);
         }
         if (logit) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int j = base + c2 + (u & 1) + (u >> 2) * 8, h = row + ((u >> 1) & 1) * 8;
-            const uint32_t k = u >> 2 ? keep1 : keep0;
-            if (h < nh && ((u & 1) ? k >> 31 : k & 1u)) logit[h * a.cap + j] = z[u >> 2][u & 3];
-          }
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int h = n * 8 + c2 + (e & 1);
+              if (h < j.nh && (e < 2 ? ok0 : ok1)) logit[h * a.cap + base + row + (e >> 1) * 8] = z[n][e];
+            }
         }
-        float mx[2];
+        float mx[NB][2];
         bool grew = false;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float x = fmaxf(fmaxf(z[0][2 * u], z[0][2 * u + 1]), fmaxf(z[1][2 * u], z[1][2 * u + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          mx[u] = fmaxf(m[u], x);
-          grew |= mx[u] > m[u];
-        }
-        if (__any_sync(0xffffffffu, grew)) {
-          float f[2];
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            f[u] = mx[u] == m[u] ? 1.f : fast_exp2(m[u] - mx[u]);
-            m[u] = mx[u];
-            l[u] *= f[u];
+            float x = fmaxf(z[n][u], z[n][2 + u]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            mx[n][u] = fmaxf(m[n][u], x);
+            grew |= mx[n][u] > m[n][u];
           }
+        if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            o[n][0] *= f[0];
-            o[n][1] *= f[0];
-            o[n][2] *= f[1];
-            o[n][3] *= f[1];
+          for (int n = 0; n < NB; ++n) {
+            float f[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              f[u] = mx[n][u] == m[n][u] ? 1.f : fast_exp2(m[n][u] - mx[n][u]);
+              m[n][u] = mx[n][u];
+              l[n][u] *= f[u];
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[n][k][e] *= f[e & 1];
           }
         }
-        uint32_t p[4];
+        uint32_t p[NB][2];  // weights as the B operand: keys (contraction) by heads
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float off = (m[u] == -INFINITY ? 0.f : m[u]) - kBias;
+        for (int n = 0; n < NB; ++n) {
           float w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[e] = fast_exp2(z[e >> 1][2 * u + (e & 1)] - off);
-          }
-          l[u] += (w[0] + w[1]) + (w[2] + w[3]);
-          p[u] = pack2<PT>(w[0], w[1]);
-          p[2 + u] = pack2<PT>(w[2], w[3]);
+          for (int e = 0; e < 4; ++e)
+            w[e] = fast_exp2(z[n][e] - ((m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1]) - kBias));
+          l[n][0] += w[0] + w[2];
+          l[n][1] += w[1] + w[3];
+          p[n][0] = movmatrix(pack2<MT>(w[0], w[1]));
+          p[n][1] = movmatrix(pack2<MT>(w[2], w[3]));
         }
-        if constexpr (!k8) {
 #pragma unroll
-          for (int n = 0; n < NT; n += 2) {
-            uint32_t b[4];
-            ldsm_x4_t(vb + S::at(r0 + ((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4)), b[0], b[1], b[2], b[3]);
+        for (int k = 0; k < KS; ++k) {
+          // 16 dims by 16 keys of V^T
+          uint32_t f[4];
+          if constexpr (!k8) {
+            ldsm_x4_t(vb + S::at(r0 + (lane >> 4) * 8 + (lane & 7), 2 * k + ((lane >> 3) & 1)), f[0], f[1], f[2], f[3]);
             if (part) {  // what lies in slots left out may be infinite or NaN
-              b[0] &= keep0;
-              b[1] &= keep1;
-              b[2] &= keep0;
-              b[3] &= keep1;
+              f[0] &= keep0;
+              f[1] &= keep0;
+              f[2] &= keep1;
+              f[3] &= keep1;
             }
-            mma<PT>(o[n], p, b[0], b[1]);
-            mma<PT>(o[n + 1], p, b[2], b[3]);
-          }
-        } else {
 #pragma unroll
-          for (int n = 0; n < NT; n += 4) {
+            for (int n = 0; n < NB; ++n) mma<MT>(o[n][k], f, p[n][0], p[n][1]);
+          } else if ((k & 1) == 0) {
             uint32_t b[4];
-            ldsm_x4_t(vb + S::at(r0 + ((lane >> 3) & 1) * 8 + (lane & 7), n / 2 + (lane >> 4)), b[0], b[1], b[2], b[3]);
+            ldsm_x4_t(vb + S::at(r0 + (lane & 15), k + (lane >> 4)), b[0], b[1], b[2], b[3]);
             if (part) {
               b[0] &= keep0;
               b[1] &= keep1;
@@ -465,15 +587,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm) attn_kernel(const AttnArgs a
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const uint32_t x = __byte_perm(b[2 * u], 0, 0x3120), y = __byte_perm(b[2 * u + 1], 0, 0x3120);
-              mma<PT>(o[n + 2 * u], p, widen2<PT>(x), widen2<PT>(y));
-              mma<PT>(o[n + 2 * u + 1], p, widen2<PT>(x >> 16), widen2<PT>(y >> 16));
+              const uint32_t f8[4] = {widen2<MT>(x), widen2<MT>(x >> 16), widen2<MT>(y), widen2<MT>(y >> 16)};
+#pragma unroll
+              for (int n = 0; n < NB; ++n) mma<MT>(o[n][k + u], f8, p[n][0], p[n][1]);
             }
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + 8 * st);
-      if (++st == S::kStages) {
+      if (++st == ST) {
         st = 0;
         phase ^= 1u;
       }
@@ -481,74 +604,83 @@ __global__ void __launch_bounds__(kThreads, kPerSm) attn_kernel(const AttnArgs a
 
     // ---- the four warps' states joined; the whole result, or a partial one
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
-      l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-      if ((lane & 3) == 0) {
-        sh.m[warp][row + 8 * u] = m[u];
-        sh.l[warp][row + 8 * u] = l[u];
-      }
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
-    float f[2];
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sh.m[w][row + 8 * u]);
-      f[u] = fast_exp2(m[u] - (M == -INFINITY ? 0.f : M));
-    }
-    const int oh = tid >> 3, od = (tid & 7) * 4;  // this thread's head and dims (of 32) in the exchange
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sh.m[w][oh]);
-#pragma unroll
-    for (int w = 0; w < kConsumers; ++w) L += sh.l[w][oh] * fast_exp2(sh.m[w][oh] - (M == -INFINITY ? 0.f : M));
-    const int64_t pslot = 2 * (int64_t)blockIdx.x + (t == t0 ? 0 : 1);
-#pragma unroll
-    for (int rd = 0; rd < D / 32; ++rd) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int dim = k8 ? (n >> 1) * 16 + 2 * c2 + 2 * (e & 1) + (n & 1) : n * 8 + c2 + (e & 1);
-          sh.x[warp][row + (e >> 1) * 8][dim] = o[rd * 4 + n][e] * f[e >> 1];
+      for (int u = 0; u < 2; ++u) {
+        float x = l[n][u];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (row == 0) {
+          sh.m[warp][n * 8 + c2 + u] = m[n][u];
+          sh.l[warp][n * 8 + c2 + u] = x;
         }
-      asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kConsumers; ++w) {
-        const float4 y = *(const float4*)&sh.x[w][oh][od];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
       }
-      if (oh < nh) {
-        if (s.whole) {
-          const float inv = L == 0.f ? 0.f : kv.v_scale / L;
+    if (!all_meet()) return gave_up();
+    constexpr int R = Sh::R;
+    const int oh = tid / (R / 4), od = (tid % (R / 4)) * 4;  // this thread's head and dims in the exchange
+    float f[NB][2];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sh.m[w][n * 8 + c2 + u]);
+        f[n][u] = fast_exp2(m[n][u] - (M == -INFINITY ? 0.f : M));
+      }
+    float M = -INFINITY, L = 0.f;
+    if (oh < Sh::H) {
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sh.m[w][oh]);
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) L += sh.l[w][oh] * fast_exp2(sh.m[w][oh] - (M == -INFINITY ? 0.f : M));
+    }
+    const int64_t pslot = 2 * (int64_t)blockIdx.x + (j.first > 0 ? 0 : 1);
+#pragma unroll
+    for (int rd = 0; rd < D / R; ++rd) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sh.x[warp][n * 8 + c2 + (e & 1)][k * 16 + (k8 ? 2 * row + (e >> 1) : row + (e >> 1) * 8)] =
+                o[n][rd * (R / 16) + k][e] * f[n][e & 1];
+      if (!all_meet()) return gave_up();
+      if (oh < j.nh) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+          const float4 y = *(const float4*)&sh.x[w][oh][od];
+          x.x += y.x;
+          x.y += y.y;
+          x.z += y.z;
+          x.w += y.w;
+        }
+        if (j.whole) {
+          const float inv = kv.v_scale / L;
           uint2 r;
           r.x = pack2<QT>(x.x * inv, x.y * inv);
           r.y = pack2<QT>(x.z * inv, x.w * inv);
           if (L == 0.f) r = make_uint2(0u, 0u);
-          *(uint2*)((uint16_t*)d.out + s.n.row * d.out_stride + (int64_t)(g * d.group + h0 + oh) * D + rd * 32 + od) = r;
+          *(uint2*)((uint16_t*)d.out + j.row * d.out_stride + (int64_t)(j.g * d.group + j.h0 + oh) * D + rd * R + od) = r;
         } else {
-          *(float4*)(a.part_o + (pslot * kHeads + oh) * D + rd * 32 + od) = x;
+          *(float4*)(a.part_o + (pslot * 16 + oh) * D + rd * R + od) = x;
         }
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+      if (!all_meet()) return gave_up();
     }
-    if ((tid & 7) == 0 && oh < nh) {
-      if (s.whole) {
+    if (od == 0 && oh < j.nh) {
+      if (j.whole) {
         const float y = L == 0.f ? -INFINITY : M + (log2f(L) - kBias);
-        const int64_t at = (int64_t)s.n.row * d.Hq + g * d.group + h0 + oh;
+        const int64_t at = (int64_t)j.row * d.Hq + j.g * d.group + j.h0 + oh;
         if (d.lse) d.lse[at] = y * 0.6931471805599453f;
         if (a.lse2) a.lse2[at] = y;
       } else {
-        a.part_ml[pslot * kHeads + oh] = make_float2(M, L);
+        a.part_ml[pslot * 16 + oh] = make_float2(M, L);
       }
     }
-    t += s.count;
   }
 }
 
@@ -566,10 +698,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
   const int e = d.sel ? r * kv.Hkv + g : r;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (h == 0 && threadIdx.x == 0 && paged_row_bad(kv, d.row_seq, d.row_len, r)) paged_err(kv, RTP_PAGED_ERANGE);
-  const int64_t tiles = a.prefix[e + 1] - a.prefix[e];
+  const int64_t units = a.prefix[e + 1] - a.prefix[e];
   uint16_t* out = (uint16_t*)d.out + r * d.out_stride + (int64_t)h * D;
   const int64_t at = (int64_t)r * d.Hq + h;
-  if (tiles == 0) {
+  if (units == 0) {
     if (threadIdx.x < D / 2) *(uint32_t*)(out + 2 * threadIdx.x) = 0u;
     if (threadIdx.x == 0) {
       if (d.lse) d.lse[at] = -INFINITY;
@@ -579,14 +711,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
   }
   const int64_t total = a.prefix[a.n_entries] * a.mult;
   const int ctas = (int)min((int64_t)grid, total);
-  const int prob = d.sel ? hh / kHeads : g * a.blocks + hh / kHeads;
-  const int64_t s0 = a.prefix[e] * a.mult + prob * tiles, s1 = s0 + tiles - 1;
+  const int heads = 8 * a.octets;
+  const int prob = d.sel ? hh / heads : g * a.blocks + hh / heads;
+  // the numbers of its first and last tile, and the CTAs that have them
+  const int64_t s1 = a.prefix[e] * a.mult + (prob + 1) * units - 1, s0 = s1 + 1 - units + kOverhead;
   int c0 = (int)(s0 * ctas / total), c1 = (int)(s1 * ctas / total);
   while (c0 + 1 < ctas && range_start(total, c0 + 1, ctas) <= s0) ++c0;
   while (c1 + 1 < ctas && range_start(total, c1 + 1, ctas) <= s1) ++c1;
   if (c0 == c1) return;  // written by its CTA
-  const int hrow = hh % kHeads;
-  const int64_t slot0 = 2 * (int64_t)c0 + (range_start(total, c0, ctas) == s0 ? 0 : 1);
+  const int hrow = hh % heads;
   __shared__ float sm[kJoinWarps], sl[kJoinWarps];
   __shared__ float so[kJoinWarps][D];
   constexpr int V = D / 32;
@@ -594,7 +727,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
 #pragma unroll
   for (int v = 0; v < V; ++v) o[v] = 0.f;
   for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
-    const int64_t p = (c == c0 ? slot0 : 2 * (int64_t)c) * kHeads + hrow;
+    const int64_t p = (2 * (int64_t)c + (c == c0 ? 1 : 0)) * 16 + hrow;
     const float2 ml = a.part_ml[p];
     float x[V];
 #pragma unroll
@@ -673,7 +806,7 @@ int device_sms() {
   return sms;
 }
 
-constexpr int kMaxSms = 160;  // what the workspace is sized for; a grid is at most kPerSm times it
+constexpr int kMaxSms = 160;  // what the workspace is sized for; a grid is at most kMaxPerSm times it
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -688,7 +821,7 @@ Layout layout_of(const rtp_paged_kv* kv, int n_rows, int n_q_heads, bool scores)
     at += align256(n);
     return x;
   };
-  const size_t parts = (size_t)2 * kPerSm * kMaxSms * kHeads;
+  const size_t parts = (size_t)2 * kMaxPerSm * kMaxSms * 16;
   l.prefix = take(((size_t)n_rows * kv->n_kv_heads + 1) * sizeof(int64_t));
   l.ml = take(parts * sizeof(float2));
   l.o = take(parts * kv->head_dim * sizeof(float));
@@ -708,24 +841,30 @@ bool map_pages(CUtensorMap* m, void* base, const int64_t* stride, const rtp_page
                     bx, bytes < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <typename QT, typename K, int D>
-cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int grid, cudaStream_t st) {
+template <typename QT, typename K, int D, int NB>
+cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   using S = Stage<K, D>;
-  constexpr size_t smem = (size_t)S::kStages * 2 * S::kHalf + 1024;
+  constexpr size_t smem = (size_t)S::stages(NB) * 2 * S::kHalf + sizeof(Shared<NB, D>);
+  static_assert((smem + 1024) * per_sm(NB) <= 228 * 1024, "the CTAs of an SM share 228 KB");
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(attn_kernel<QT, K, D>, smem, done);
+  cudaError_t e = allow_smem(attn_kernel<QT, K, D, NB>, smem, done);
   if (e != cudaSuccess) return e;
+  const int64_t slots = a.d.sel ? a.d.sel_stride * a.d.kv.page_size : a.cap;
+  const int64_t most = (int64_t)a.n_entries * a.mult * ((slots + kTile - 1) / kTile + kOverhead);
+  const int sms = device_sms();
+  int64_t grid = (int64_t)per_sm(NB) * (sms < kMaxSms ? sms : kMaxSms);
+  if (grid > most) grid = most;
   if (a.n_entries > kInline) {
     plan_kernel<<<1, 1024, 0, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_after(attn_kernel<QT, K, D>, dim3(grid), kThreads, smem, st, a, km, vm);
+    e = launch_after(attn_kernel<QT, K, D, NB>, dim3((unsigned)grid), kThreads, smem, st, a, km, vm);
   } else {
-    attn_kernel<QT, K, D><<<grid, kThreads, smem, st>>>(a, km, vm);
+    attn_kernel<QT, K, D, NB><<<(unsigned)grid, kThreads, smem, st>>>(a, km, vm);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
   const float bias = std::is_same_v<K, __nv_bfloat16> ? 0.f : 15.f;
-  e = launch_after(join_kernel<QT, D>, dim3(a.d.Hq, a.d.n_rows), kJoinWarps * 32, 0, st, a, grid, bias);
+  e = launch_after(join_kernel<QT, D>, dim3(a.d.Hq, a.d.n_rows), kJoinWarps * 32, 0, st, a, (int)grid, bias);
   if (e != cudaSuccess || !a.logits) return e;
   const int64_t blocks = (a.cap + 1023) / 1024;
   return launch_after(weights_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024), a.d.kv.Hkv, a.d.n_rows), 256, 0,
@@ -733,8 +872,10 @@ cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
 }
 
 template <typename QT, typename K>
-cudaError_t run_d(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int grid, cudaStream_t st) {
-  return a.d.kv.D == 64 ? run<QT, K, 64>(a, km, vm, grid, st) : run<QT, K, 128>(a, km, vm, grid, st);
+cudaError_t run_d(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  if (a.octets == 1)
+    return a.d.kv.D == 64 ? run<QT, K, 64, 1>(a, km, vm, st) : run<QT, K, 128, 1>(a, km, vm, st);
+  return a.d.kv.D == 64 ? run<QT, K, 64, 2>(a, km, vm, st) : run<QT, K, 128, 2>(a, km, vm, st);
 }
 
 }  // namespace
@@ -746,7 +887,8 @@ size_t paged_decode_workspace(const rtp_paged_kv* kv, int n_rows, int n_q_heads,
 cudaError_t launch_paged_decode(const DecodeArgs& d, const rtp_paged_kv* kv, int qt, cudaStream_t st) {
   AttnArgs a{};
   a.d = d;
-  a.blocks = (d.group + kHeads - 1) / kHeads;
+  a.octets = d.group <= 8 ? 1 : 2;
+  a.blocks = (d.group + 8 * a.octets - 1) / (8 * a.octets);
   a.box = kv->page_size < kTile ? kv->page_size : kTile;
   a.n_entries = d.sel ? d.n_rows * kv->n_kv_heads : d.n_rows;
   a.mult = d.sel ? a.blocks : kv->n_kv_heads * a.blocks;
@@ -763,16 +905,11 @@ cudaError_t launch_paged_decode(const DecodeArgs& d, const rtp_paged_kv* kv, int
   CUtensorMap km, vm;
   if (!map_pages(&km, kv->k, kv->k_stride, kv, a.box) || !map_pages(&vm, kv->v, kv->v_stride, kv, a.box))
     return cudaErrorInvalidValue;
-  const int64_t slots = d.sel ? (int64_t)d.sel_stride * kv->page_size : a.cap;
-  const int64_t most = (int64_t)a.n_entries * a.mult * ((slots + kTile - 1) / kTile);
-  const int sms = device_sms();
-  int64_t grid = (int64_t)kPerSm * (sms < kMaxSms ? sms : kMaxSms);
-  if (grid > most) grid = most;
   const int kt = kv->dtype;
-  if (qt == RTP_FP16 && kt == RTP_FP16) return run_d<__half, __half>(a, km, vm, (int)grid, st);
-  if (qt == RTP_BF16 && kt == RTP_BF16) return run_d<__nv_bfloat16, __nv_bfloat16>(a, km, vm, (int)grid, st);
-  if (qt == RTP_FP16) return run_d<__half, __nv_fp8_e4m3>(a, km, vm, (int)grid, st);
-  return run_d<__nv_bfloat16, __nv_fp8_e4m3>(a, km, vm, (int)grid, st);
+  if (qt == RTP_FP16 && kt == RTP_FP16) return run_d<__half, __half>(a, km, vm, st);
+  if (qt == RTP_BF16 && kt == RTP_BF16) return run_d<__nv_bfloat16, __nv_bfloat16>(a, km, vm, st);
+  if (qt == RTP_FP16) return run_d<__half, __nv_fp8_e4m3>(a, km, vm, st);
+  return run_d<__nv_bfloat16, __nv_fp8_e4m3>(a, km, vm, st);
 }
 
 }  // namespace rtp

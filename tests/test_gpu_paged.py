@@ -611,3 +611,33 @@ def test_select_close_scores():
 def test_evict_beyond_shared_memory():
     c = Case([50000, 70], hq=1, hkv=1, d=64, page=16, kv="e4m3", seed=1)
     run_evict(c, 20000, 100, 4, 3, ties=True)
+
+
+def test_decode_e4m3_query_ranges():
+    """bf16 queries far outside fp16's range over e4m3 pages: scaled per head, not rounded."""
+    c = Case([130, 77], hq=4, hkv=2, d=128, page=32, kv="e4m3", q="bf16", seed=14, k_scale=2.0**-30)
+    q = c.randn(2, 4, 128)
+    q *= torch.tensor([2.0**30, 2.0**25, 2.0**-60, 2.0**33])[None, :, None]
+    q = q.to(c.qt).to(c.device)
+    c.k = c.put(torch.nan_to_num(c.randn(c.pool, 2, 32, 128) * 20))
+    c.v = c.put(c.randn(c.pool, 2, 32, 128))
+    out, lse = c.cache().decode(q, c.ints(c.lens), sm_scale=0.002, return_lse=True)
+    check_decode(c, q, out, lse, [(b, np.arange(n)) for b, n in enumerate(c.lens)], scale=float(np.float32(0.002)))
+
+
+def test_decode_nan_query_gives_nan():
+    c = Case([200, 200], hq=16, hkv=2, d=64, page=16, kv="bf16", seed=15)
+    q = c.randn(2, 16, 64).to(c.qt).to(c.device)
+    q[1, 3, 7] = math.nan
+    out, lse = c.cache().decode(q, c.ints([200, 200]), return_lse=True)
+    o = f64(out)
+    assert np.isnan(o[1, 3]).all() and bool(lse[1, 3].isnan())
+    assert np.isfinite(o[0]).all() and np.isfinite(np.delete(o[1], 3, 0)).all()
+
+
+def test_decode_many_ragged_rows():
+    """More rows than every CTA plans by itself, empty ones among them, split ones too."""
+    r = np.random.default_rng(8)
+    lens = np.where(r.random(700) < 0.3, 0, r.integers(1, 60, 700))
+    lens[123], lens[699] = 9000, 3000
+    run_decode(Case(lens.tolist(), hq=3, hkv=1, d=64, page=16, kv="fp16", seed=16))
