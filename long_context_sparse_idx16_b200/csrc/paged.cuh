@@ -34,6 +34,14 @@ struct PagedView {
   uint32_t* err;
 };
 
+// Every kernel of these operators is launched so that it may start while the one before it drains
+// (launch_after), and calls this before it touches global memory: it lets the next one start and
+// waits until the one before has finished.
+__device__ __forceinline__ void after_wait() {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ void paged_err(const PagedView& p, uint32_t bit) {
   if (p.err) atomicOr(p.err, bit);
 }
@@ -278,8 +286,7 @@ struct EvictArgs {
   int32_t* n_moves; // workspace [n_seqs][Hkv]
 };
 
-// Launch that may start while the kernel before it drains; it waits (griddepcontrol.wait) before
-// it reads what that kernel wrote.
+// Launch that may start while the kernel before it in the stream drains (see after_wait).
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t c = {};

@@ -5,11 +5,13 @@
 //   z_c = y_c cos - y_{c+D/2} sin, z_{c+D/2} = y_{c+D/2} cos + y_c sin, angle = pos * theta_c.
 // The angle is formed and reduced in fp64 (rope_cos_sin); the rest is fp32.
 //
-// Every row is read once and written once, so HBM bounds a chunk and launch latency a decode step.
-// A warp takes one token and a run of its heads: the D/8 lanes of a row hold four dims of each half
-// (the two members of four rotation pairs), so norm and rotation need no shared memory, and the
-// sines and cosines stay in registers for all heads of the run.  The runs are as long as still
-// leaves enough warps (the host picks), since every warp forms the angles again.
+// Every row is read once and written once, so HBM bounds a chunk and launch latency a decode step;
+// what stands between is instructions.  A warp takes one token and a run of its row groups (as many
+// rows as it holds at once, all of q, of k or of v).  A lane holds eight dims of each half of a row,
+// the two members of eight rotation pairs: 16-byte loads and stores, norm and rotation without
+// shared memory, two fp32 values an instruction (fma.f32x2).  The sines and cosines are formed once
+// per warp, shared out over the lanes that need the same ones.  The runs are as long as still leaves
+// enough warps to fill the GPU (the host picks), since every warp forms the angles again.
 // One token per sequence: the K rows' warps also widen the page bounds.  In a chunk a page gets
 // several rows: a second kernel takes its bounds from the rows just written (in L2).
 #include "paged.cuh"
@@ -19,7 +21,145 @@ namespace rtp {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kUnroll = 4;  // row groups in flight per warp
+
+// ---- two fp32 values in one register pair
+
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack(f2 r, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// 16-bit pair to fp32 pair
+template <typename T>
+__device__ __forceinline__ f2 widen(uint32_t u) {
+  if constexpr (std::is_same_v<T, __half>) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+    return pack(f.x, f.y);
+  } else {
+    return pack(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void widen8(uint4 u, f2* y) {
+  y[0] = widen<T>(u.x);
+  y[1] = widen<T>(u.y);
+  y[2] = widen<T>(u.z);
+  y[3] = widen<T>(u.w);
+}
+
+// Eight values to K: 16 bytes of 16-bit values, or 8 of e4m3 (nearest, saturating).
+template <typename K>
+struct Pack8;
+template <>
+struct Pack8<__nv_fp8_e4m3> {
+  using type = uint2;
+  static __device__ __forceinline__ uint2 of(const f2* y) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 f;
+      unpack(y[i], f.x, f.y);
+      w[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+  }
+};
+template <typename T>
+struct Pack8 {
+  using type = uint4;
+  static __device__ __forceinline__ uint4 of(const f2* y) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      unpack(y[i], a, b);
+      w[i] = pack2<T>(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// Least and greatest of stored values, eight at a time, as 16-bit pairs (e4m3: as fp16, exactly).
+// A NaN yields to the other value.
+template <typename K>
+struct Range8 {
+  using T = std::conditional_t<sizeof(K) == 1, __half, K>;
+  using Raw = typename Pack8<K>::type;
+  using V2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+  uint32_t lo[4], hi[4];
+  static __device__ __forceinline__ V2 v(uint32_t x) { return *reinterpret_cast<V2*>(&x); }
+  static __device__ __forceinline__ uint32_t u(V2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+  static __device__ __forceinline__ void wide(Raw r, uint32_t* w) {
+    if constexpr (sizeof(K) == 1) {
+      w[0] = widen2<T>(r.x);
+      w[1] = widen2<T>(r.x >> 16);
+      w[2] = widen2<T>(r.y);
+      w[3] = widen2<T>(r.y >> 16);
+    } else {
+      w[0] = r.x;
+      w[1] = r.y;
+      w[2] = r.z;
+      w[3] = r.w;
+    }
+  }
+  static __device__ __forceinline__ Raw narrow(const uint32_t* w) {
+    if constexpr (sizeof(K) == 1) {
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2_raw x = *reinterpret_cast<const __half2_raw*>(&w[i]);
+        h[i] = __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+      }
+      return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    } else {
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ void none() {
+    const uint32_t inf = std::is_same_v<T, __half> ? 0x7c007c00u : 0x7f807f80u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = inf;
+      hi[i] = inf | 0x80008000u;
+    }
+  }
+  __device__ __forceinline__ void add(const uint32_t* l, const uint32_t* h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = u(__hmin2(v(lo[i]), v(l[i])));
+      hi[i] = u(__hmax2(v(hi[i]), v(h[i])));
+    }
+  }
+  __device__ __forceinline__ void row(Raw r) {
+    uint32_t w[4];
+    wide(r, w);
+    add(w, w);
+  }
+  // the stored bounds, D values apart
+  __device__ __forceinline__ void stored(const K* p, int D) {
+    uint32_t l[4], h[4];
+    wide(*(const Raw*)p, l);
+    wide(*(const Raw*)(p + D), h);
+    add(l, h);
+  }
+  __device__ __forceinline__ void store(K* p, int D) const {
+    *(Raw*)p = narrow(lo);
+    *(Raw*)(p + D) = narrow(hi);
+  }
+};
 
 // Sequence of token t: the last b with cu[b] <= t.
 __device__ __forceinline__ int token_seq(const int32_t* cu, int n_seqs, int t) {
@@ -32,49 +172,17 @@ __device__ __forceinline__ int token_seq(const int32_t* cu, int n_seqs, int t) {
   return lo;
 }
 
-template <typename T>
-__device__ __forceinline__ void unpack4(uint2 u, float* f) {
-  const T* h = reinterpret_cast<const T*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = to_f32(h[i]);
-}
-
-// Four values to 16 bits (8 bytes) or e4m3 (4 bytes).
-template <typename K>
-__device__ __forceinline__ void store4(void* at, const float* f) {
-  if constexpr (sizeof(K) == 1) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
-    *(uint32_t*)at = lo | hi << 16;
-  } else {
-    K h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = from_f32<K>(f[i]);
-    *(uint2*)at = *reinterpret_cast<const uint2*>(h);
-  }
-}
-
-template <typename K>
-__device__ __forceinline__ void load4(const void* at, float* f) {
-  if constexpr (sizeof(K) == 1) {
-    const uint32_t u = *(const uint32_t*)at;
-    const __nv_fp8_e4m3* h = reinterpret_cast<const __nv_fp8_e4m3*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = to_f32(h[i]);
-  } else {
-    unpack4<K>(*(const uint2*)at, f);
-  }
-}
-
-// Units: heads 0 .. Hq-1 are q, then Hkv of k, then Hkv of v.  `run` units per warp.
-template <typename T, typename K, int D>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a, int run, int runs, bool widen) {
-  constexpr int L = D / 8;        // lanes of a row
+// Row groups of a token: ceil(Hq / R) of q, then ceil(Hkv / R) of k, then as many of v; `run` of them
+// per warp.  U groups are in flight at once.
+template <typename T, typename K, int D, int U>
+__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a, int run, int runs, bool widen_bounds) {
+  constexpr int L = D / 16;       // lanes of a row
   constexpr int R = 32 / L;       // rows a warp holds at once
   constexpr int H = D / 2;
   const PagedView& kv = a.kv;
   const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = (int)(task / runs), lane = threadIdx.x & 31, sub = lane / L, c = (lane % L) * 4;
+  const int t = (int)(task / runs), lane = threadIdx.x & 31, sub = lane / L, c = (lane % L) * 8;
+  after_wait();
   if (t >= a.n_tokens) return;
   int b = t, i = 0;
   if (a.cu_new) {
@@ -82,102 +190,134 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
     b = token_seq(a.cu_new, kv.n_seqs, t);
     i = t - a.cu_new[b];
   }
-  const int u0 = (int)(task % runs) * run, units = a.Hq + 2 * kv.Hkv, u1 = min(u0 + run, units);
+  const int gq = (a.Hq + R - 1) / R, gk = (kv.Hkv + R - 1) / R;
+  const int u0 = (int)(task % runs) * run, u1 = min(u0 + run, gq + 2 * gk);
+  const auto load = [&](int u, uint4* x) {
+    const bool is_q = u < gq, is_v = u >= gq + gk;
+    const int h = (u - (is_q ? 0 : is_v ? gq + gk : gq)) * R + sub;
+    const T* p = (is_q ? (const T*)a.q + t * a.q_stride : is_v ? (const T*)a.v + t * a.v_stride : (const T*)a.k + t * a.k_stride) +
+                 (int64_t)h * D + c;
+    x[0] = x[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (u < u1 && h < (is_q ? a.Hq : kv.Hkv)) {
+      x[0] = *(const uint4*)p;
+      x[1] = *(const uint4*)(p + H);
+    }
+  };
+  uint4 x[U][2];
+#pragma unroll
+  for (int n = 0; n < U; ++n) load(u0 + n, x[n]);
   const int64_t slot = (int64_t)a.seq_len[b] + i;
   const int pos = a.positions ? a.positions[t] : (int)slot;
   int64_t page = -1;
-  if (u1 > a.Hq) {
+  if (u1 > gq) {
     if (slot >= 0 && slot < ((int64_t)kv.max_pages << kv.page_shift))
       page = paged_page(kv, b, (int)(slot >> kv.page_shift));
     if (page < 0 && lane == 0) paged_err(kv, RTP_PAGED_ERANGE);
   }
   const int off = (int)(slot & (kv.page_size - 1));
-  float cs[4], sn[4];
-  if (u0 < a.Hq + kv.Hkv) {
+  // this lane's eight angles: the R lanes of equal c form 8 / R of them each
+  f2 cs[4], sn[4], wt[2][4];
+  if (u0 < gq + gk) {
+    constexpr int N = 8 / R > 0 ? 8 / R : 1;
+    float cc[N], ss[N];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) rope_cos_sin(pos, a.theta[c + e], &cs[e], &sn[e]);
+    for (int e = 0; e < N; ++e) rope_cos_sin(pos, a.theta[c + (sub * N + e) % 8], &cc[e], &ss[e]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int s0 = (2 * e) / N, s1 = (2 * e + 1) / N;
+      cs[e] = pack(__shfl_sync(0xffffffffu, cc[(2 * e) % N], s0 * L + lane % L),
+                   __shfl_sync(0xffffffffu, cc[(2 * e + 1) % N], s1 * L + lane % L));
+      sn[e] = pack(__shfl_sync(0xffffffffu, ss[(2 * e) % N], s0 * L + lane % L),
+                   __shfl_sync(0xffffffffu, ss[(2 * e + 1) % N], s1 * L + lane % L));
+    }
   }
-  for (int v0 = u0; v0 < u1; v0 += R * kUnroll) {
-    uint2 x[kUnroll][2];
+  const void* have = nullptr;  // the weights in wt
+#pragma unroll 1
+  for (int v0 = u0; v0 < u1; v0 += U) {
+    uint4 y[U][2];
 #pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
-      const int u = v0 + n * R + sub;
-      if (u < u1) {
-        const T* p = u < a.Hq            ? (const T*)a.q + t * a.q_stride + (int64_t)u * D
-                     : u < a.Hq + kv.Hkv ? (const T*)a.k + t * a.k_stride + (int64_t)(u - a.Hq) * D
-                                         : (const T*)a.v + t * a.v_stride + (int64_t)(u - a.Hq - kv.Hkv) * D;
-        x[n][0] = *(const uint2*)(p + c);
-        x[n][1] = *(const uint2*)(p + H + c);
-      } else {
-        x[n][0] = x[n][1] = make_uint2(0u, 0u);
-      }
+    for (int n = 0; n < U; ++n) {
+      y[n][0] = x[n][0];
+      y[n][1] = x[n][1];
+    }
+    if (v0 + U < u1) {
+#pragma unroll
+      for (int n = 0; n < U; ++n) load(v0 + U + n, x[n]);
     }
 #pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
-      const int u = v0 + n * R + sub;
-      const bool is_q = u < a.Hq, is_v = u >= a.Hq + kv.Hkv;
-      float y[8];
-      unpack4<T>(x[n][0], y);
-      unpack4<T>(x[n][1], y + 4);
-      const T* w = (const T*)(is_q ? a.q_weight : a.k_weight);
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(y[e], y[e], s);
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (u >= u1) continue;
+    for (int n = 0; n < U; ++n) {
+      const int u = v0 + n;
+      if (u >= u1) break;  // the whole warp alike
+      const bool is_q = u < gq, is_v = u >= gq + gk;
+      const int h = (u - (is_q ? 0 : is_v ? gq + gk : gq)) * R + sub;
+      f2 z[2][4];
+      widen8<T>(y[n][0], z[0]);
+      widen8<T>(y[n][1], z[1]);
       if (!is_v) {
+        const T* w = (const T*)(is_q ? a.q_weight : a.k_weight);
         if (w) {
-          const float r = rsqrtf(s * (1.f / D) + a.eps);
-          float g[8];
-          unpack4<T>(*(const uint2*)(w + c), g);
-          unpack4<T>(*(const uint2*)(w + H + c), g + 4);
+          f2 s2 = mul2(z[0][0], z[0][0]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = y[e] * r * g[e];
+          for (int e = 1; e < 8; ++e) s2 = fma2(z[e >> 2][e & 3], z[e >> 2][e & 3], s2);
+          float s, s1;
+          unpack(s2, s, s1);
+          s += s1;
+#pragma unroll
+          for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          const float r = rsqrtf(s * (1.f / D) + a.eps);
+          const f2 r2 = pack(r, r);
+          if (w != have) {
+            widen8<T>(*(const uint4*)(w + c), wt[0]);
+            widen8<T>(*(const uint4*)(w + H + c), wt[1]);
+            have = w;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e >> 2][e & 3] = mul2(mul2(z[e >> 2][e & 3], r2), wt[e >> 2][e & 3]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float y0 = y[e], y1 = y[e + 4];
-          y[e] = y0 * cs[e] - y1 * sn[e];
-          y[e + 4] = y1 * cs[e] + y0 * sn[e];
+          const f2 z0 = z[0][e], z1 = z[1][e];
+          float n0, n1;
+          unpack(mul2(z1, sn[e]), n0, n1);
+          z[0][e] = fma2(z0, cs[e], pack(-n0, -n1));
+          z[1][e] = fma2(z1, cs[e], mul2(z0, sn[e]));
         }
       }
+      if (h >= (is_q ? a.Hq : kv.Hkv)) continue;
       if (is_q) {
-        T* o = (T*)a.q_out + t * a.q_out_stride + (int64_t)u * D;
-        store4<T>(o + c, y);
-        store4<T>(o + H + c, y + 4);
+        T* o = (T*)a.q_out + t * a.q_out_stride + (int64_t)h * D + c;
+        *(uint4*)o = Pack8<T>::of(z[0]);
+        *(uint4*)(o + H) = Pack8<T>::of(z[1]);
       } else if (page >= 0) {
-        const int g = u - a.Hq - (is_v ? kv.Hkv : 0);
-        K* o = (K*)(is_v ? kv.v + page * kv.vp + g * kv.vh + off * kv.vs : kv.k + page * kv.kp + g * kv.kh + off * kv.ks);
+        K* o = (K*)(is_v ? kv.v + page * kv.vp + h * kv.vh + off * kv.vs : kv.k + page * kv.kp + h * kv.kh + off * kv.ks) + c;
         const float f = is_v ? kv.v_scale : kv.k_scale;
         if (f != 1.f) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = y[e] / f;
+          for (int e = 0; e < 8; ++e) {
+            float p, q;
+            unpack(z[e >> 2][e & 3], p, q);
+            z[e >> 2][e & 3] = pack(p / f, q / f);
+          }
         }
-        store4<K>(o + c, y);
-        store4<K>(o + H + c, y + 4);
+        const auto k0 = Pack8<K>::of(z[0]), k1 = Pack8<K>::of(z[1]);
+        using Raw = typename Pack8<K>::type;
+        *(Raw*)o = k0;
+        *(Raw*)(o + H) = k1;
         if (!is_v) {
-          if (c == 0 && a.slot_pos) a.slot_pos[((int64_t)b * kv.Hkv + g) * a.slot_pos_stride + slot] = pos;
-          if (widen) {  // the page's only new row
-            K* lim = (K*)kv.bounds + ((page * kv.Hkv + g) * 2) * D;
-            float lo[8], hi[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = to_f32(from_f32<K>(y[e]));  // the key as it was stored
+          if (c == 0 && a.slot_pos) a.slot_pos[((int64_t)b * kv.Hkv + h) * a.slot_pos_stride + slot] = pos;
+          if (widen_bounds) {  // the page's only new row
+            K* lim = (K*)kv.bounds + ((page * kv.Hkv + h) * 2) * D + c;
+            Range8<K> r0, r1;
+            r0.none();
+            r1.none();
             if (off > 0) {
-              load4<K>(lim + c, lo);
-              load4<K>(lim + H + c, lo + 4);
-              load4<K>(lim + D + c, hi);
-              load4<K>(lim + D + H + c, hi + 4);
+              r0.stored(lim, D);
+              r1.stored(lim + H, D);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              lo[e] = fminf(off > 0 ? lo[e] : INFINITY, y[e]);
-              hi[e] = fmaxf(off > 0 ? hi[e] : -INFINITY, y[e]);
-            }
-            store4<K>(lim + c, lo);
-            store4<K>(lim + H + c, lo + 4);
-            store4<K>(lim + D + c, hi);
-            store4<K>(lim + D + H + c, hi + 4);
+            r0.row(k0);
+            r1.row(k1);
+            r0.store(lim, D);
+            r1.store(lim + H, D);
           }
         }
       }
@@ -185,64 +325,50 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
   }
 }
 
-// Bounds of page `i` of sequence b for KV head g over slots [first, last) of it, by one warp-sized
-// group of rows: lanes hold four dims each, the CTA's row groups take every R-th slot.  `widen`:
-// from the stored bounds on, unless slot 0 is among them.
+// Bounds of page `i` of sequence b for KV head g over slots [first, last) of it: lanes hold eight
+// dims each, the CTA's row groups take every R-th slot.  `widen`: from the stored bounds on, unless
+// slot 0 is among them.
 constexpr int kBoundThreads = 128;
 
 template <typename K, int D>
 __device__ void bounds_of(const PagedView& kv, int b, int i, int g, int first, int last, bool widen,
-                          float (*sh)[2][D]) {
-  constexpr int L = D / 4;                 // lanes of a row
-  constexpr int R = kBoundThreads / L;     // rows at once
-  const int c = (threadIdx.x % L) * 4, r = threadIdx.x / L;
+                          uint32_t (*sh)[2][D / 2]) {
+  constexpr int L = D / 8;                 // lanes of a row
+  constexpr int R = kBoundThreads / L;     // rows at once: 8 or 16
+  using Raw = typename Pack8<K>::type;
+  const int c = (threadIdx.x % L) * 8, r = threadIdx.x / L;
   const int64_t page = paged_page(kv, b, i);
   if (page < 0) {
     if (threadIdx.x == 0) paged_err(kv, RTP_PAGED_ERANGE);
     return;
   }
-  K* o = (K*)kv.bounds + ((page * kv.Hkv + g) * 2) * D;
-  float lo[4], hi[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    lo[e] = INFINITY;
-    hi[e] = -INFINITY;
-  }
-  if (widen && first > 0 && r == 0) {
-    load4<K>(o + c, lo);
-    load4<K>(o + D + c, hi);
-  }
+  K* o = (K*)kv.bounds + ((page * kv.Hkv + g) * 2) * D + c;
+  Range8<K> m;
+  m.none();
+  if (widen && first > 0 && r == 0) m.stored(o, D);
   const uint8_t* row = kv.k + page * kv.kp + g * kv.kh;
-#pragma unroll 4
-  for (int s = first + r; s < last; s += R) {
-    float x[4];
-    load4<K>((const K*)(row + s * kv.ks) + c, x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      lo[e] = fminf(lo[e], x[e]);
-      hi[e] = fmaxf(hi[e], x[e]);
-    }
-  }
+#pragma unroll 8
+  for (int s = first + r; s < last; s += R) m.row(*(const Raw*)((const K*)(row + s * kv.ks) + c));
   __syncthreads();  // the last page's exchange has been read
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    sh[r][0][c + e] = lo[e];
-    sh[r][1][c + e] = hi[e];
+    sh[r][0][c / 2 + e] = m.lo[e];
+    sh[r][1][c / 2 + e] = m.hi[e];
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < 2 * D; x += kBoundThreads) {
-    float y = sh[0][x / D][x % D];
+  if (r == 0) {
 #pragma unroll
-    for (int n = 1; n < R; ++n) y = x < D ? fminf(y, sh[n][0][x]) : fmaxf(y, sh[n][1][x - D]);
-    o[x] = from_f32<K>(y);
+    for (int n = 1; n < R; ++n) m.add(&sh[n][0][c / 2], &sh[n][1][c / 2]);
+    m.store(o, D);
   }
 }
 
 template <typename K, int D>
 __global__ void __launch_bounds__(kBoundThreads) append_bounds_kernel(const AppendArgs a) {
-  __shared__ float sh[kBoundThreads * 4 / D][2][D];
+  __shared__ uint32_t sh[kBoundThreads * 8 / D][2][D / 2];
   const PagedView& kv = a.kv;
   const int b = blockIdx.z;
+  after_wait();
   const int n = a.cu_new[b + 1] - a.cu_new[b];
   const int64_t cap = (int64_t)kv.max_pages << kv.page_shift;
   const int64_t s0 = a.seq_len[b], s1 = min(s0 + n, cap);
@@ -256,7 +382,8 @@ __global__ void __launch_bounds__(kBoundThreads) append_bounds_kernel(const Appe
 
 template <typename K, int D>
 __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const PagedView kv, const int32_t* seq_len) {
-  __shared__ float sh[kBoundThreads * 4 / D][2][D];
+  __shared__ uint32_t sh[kBoundThreads * 8 / D][2][D / 2];
+  after_wait();
   const int b = blockIdx.z;
   int seq;
   const int n = paged_row(kv, nullptr, seq_len, b, &seq);
@@ -265,27 +392,27 @@ __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const PagedView k
     bounds_of<K, D>(kv, b, i, blockIdx.y, 0, min(kv.page_size, n - (i << kv.page_shift)), false, sh);
 }
 
-// Units per warp: all of a token's in a large chunk (one set of angles per token), fewer while the
-// warps would not fill the GPU (64 warps on each of 148 SMs), but no less than a warp holds at once.
-int units_per_warp(int64_t tokens, int units, int at_once) {
-  const int64_t want = 148 * 64;
-  int run = units;
-  while (run > at_once && tokens * ((units + run - 1) / run) < want) run = (run + 1) / 2;
-  return (run + at_once - 1) / at_once * at_once;
+// Row groups per warp: all of a token's in a large chunk (one set of angles per token), fewer while
+// the warps would not fill the GPU (16 on each of 148 SMs).
+int groups_per_warp(int64_t tokens, int groups) {
+  int run = groups;
+  while (run > 1 && tokens * ((groups + run - 1) / run) < 148 * 16) run = (run + 1) / 2;
+  return run;
 }
 
 template <typename T, typename K, int D>
 cudaError_t run_append(const AppendArgs& a, cudaStream_t st) {
-  const int units = a.Hq + 2 * a.kv.Hkv, run = units_per_warp(a.n_tokens, units, 256 / D);
-  const int runs = (units + run - 1) / run;
+  constexpr int R = 512 / D;
+  const int groups = (a.Hq + R - 1) / R + 2 * ((a.kv.Hkv + R - 1) / R), run = groups_per_warp(a.n_tokens, groups);
+  const int runs = (groups + run - 1) / run;
   const int64_t warps = (int64_t)a.n_tokens * runs;
   const bool one = !a.cu_new && a.kv.bounds;
-  append_kernel<T, K, D><<<(unsigned)((warps + kWarps - 1) / kWarps), 32 * kWarps, 0, st>>>(a, run, runs, one);
-  const cudaError_t e = cudaGetLastError();
+  const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps));
+  const cudaError_t e = run == 1 ? launch_after(append_kernel<T, K, D, 1>, grid, 32 * kWarps, 0, st, a, run, runs, one)
+                                 : launch_after(append_kernel<T, K, D, 2>, grid, 32 * kWarps, 0, st, a, run, runs, one);
   if (e != cudaSuccess || !a.kv.bounds || one) return e;
-  const dim3 grid(a.max_new / a.kv.page_size + 2, a.kv.Hkv, a.kv.n_seqs);
-  append_bounds_kernel<K, D><<<grid, kBoundThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  const dim3 pages(a.max_new / a.kv.page_size + 2, a.kv.Hkv, a.kv.n_seqs);
+  return launch_after(append_bounds_kernel<K, D>, pages, kBoundThreads, 0, st, a);
 }
 
 template <typename T, typename K>
@@ -296,9 +423,8 @@ cudaError_t run_append_d(const AppendArgs& a, cudaStream_t st) {
 template <typename K>
 cudaError_t run_bounds(const PagedView& kv, const int32_t* seq_len, cudaStream_t st) {
   const dim3 grid(kv.max_pages < 1024 ? kv.max_pages : 1024, kv.Hkv, kv.n_seqs);
-  if (kv.D == 64) bounds_kernel<K, 64><<<grid, kBoundThreads, 0, st>>>(kv, seq_len);
-  else bounds_kernel<K, 128><<<grid, kBoundThreads, 0, st>>>(kv, seq_len);
-  return cudaGetLastError();
+  if (kv.D == 64) return launch_after(bounds_kernel<K, 64>, grid, kBoundThreads, 0, st, kv, seq_len);
+  return launch_after(bounds_kernel<K, 128>, grid, kBoundThreads, 0, st, kv, seq_len);
 }
 
 }  // namespace

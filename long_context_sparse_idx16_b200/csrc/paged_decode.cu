@@ -46,6 +46,7 @@ constexpr int kInline = 256;      // entries whose tile prefix every CTA forms b
 constexpr int kNoSlot = 0x7fff8000;  // beyond every length: a box none of whose slots is attended
 constexpr int kOverhead = 2;      // tiles' worth of time that a problem costs besides its tiles
 constexpr int kMaxPerSm = 3;
+constexpr int kMaxSms = 160;      // what the workspace is sized for; a grid is at most kMaxPerSm times it
 
 // Eight query heads need half the registers of sixteen: three CTAs per SM instead of two, with
 // rings of 64 KB instead of 96 KB.
@@ -160,6 +161,7 @@ __device__ __forceinline__ void tile_prefix(const AttnArgs& a, int64_t* out, int
 // More entries than kInline: one CTA writes the prefix for everybody.
 __global__ void __launch_bounds__(1024) plan_kernel(const AttnArgs a) {
   __shared__ int64_t sums[32];
+  after_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t run = 0;
   for (int e0 = 0; e0 < a.n_entries; e0 += 1024) {
@@ -267,6 +269,11 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
   const uint32_t job_full = smem_u32(&sh.job_full), job_empty = smem_u32(&sh.job_empty), meet = smem_u32(&sh.meet);
   volatile int* stop = &sh.stop;
   const bool inl = a.n_entries <= kInline;
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&km) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&vm) : "memory");
+  }
+  after_wait();
   if (warp == kConsumers) {
     if (lane == 0) {
       for (int i = 0; i < ST; ++i) {
@@ -282,8 +289,6 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
   } else if (warp == 0) {
     if (inl) tile_prefix(a, sh.prefix, lane);
   }
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (!inl) asm volatile("griddepcontrol.wait;" ::: "memory");  // plan_kernel's prefix
   __syncthreads();
   const int64_t* prefix = inl ? sh.prefix : a.prefix;
   if (inl && blockIdx.x == 0)
@@ -686,84 +691,105 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
 
 // One CTA per (query head, row): the partial results of a problem that crosses CTAs, in CTA order;
 // zeros for a row without slots.
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
 
 template <typename QT, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a, int grid, float bias) {
-  asm volatile("griddepcontrol.launch_dependents;");
   const DecodeArgs& d = a.d;
   const PagedView& kv = d.kv;
   const int h = blockIdx.x, r = blockIdx.y, g = h / d.group, hh = h % d.group;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int e = d.sel ? r * kv.Hkv + g : r;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (h == 0 && threadIdx.x == 0 && paged_row_bad(kv, d.row_seq, d.row_len, r)) paged_err(kv, RTP_PAGED_ERANGE);
-  const int64_t units = a.prefix[e + 1] - a.prefix[e];
+  __shared__ float weight[kMaxPerSm * kMaxSms];
+  __shared__ float red[2][kJoinWarps];
+  __shared__ float so[kJoinWarps][D];
+  after_wait();
+  if (h == 0 && tid == 0 && paged_row_bad(kv, d.row_seq, d.row_len, r)) paged_err(kv, RTP_PAGED_ERANGE);
+  const int64_t start = a.prefix[e], units = a.prefix[e + 1] - start, all = a.prefix[a.n_entries];
   uint16_t* out = (uint16_t*)d.out + r * d.out_stride + (int64_t)h * D;
   const int64_t at = (int64_t)r * d.Hq + h;
   if (units == 0) {
-    if (threadIdx.x < D / 2) *(uint32_t*)(out + 2 * threadIdx.x) = 0u;
-    if (threadIdx.x == 0) {
+    if (tid < D / 2) *(uint32_t*)(out + 2 * tid) = 0u;
+    if (tid == 0) {
       if (d.lse) d.lse[at] = -INFINITY;
       if (a.lse2) a.lse2[at] = -INFINITY;
     }
     return;
   }
-  const int64_t total = a.prefix[a.n_entries] * a.mult;
+  const int64_t total = all * a.mult;
   const int ctas = (int)min((int64_t)grid, total);
   const int heads = 8 * a.octets;
   const int prob = d.sel ? hh / heads : g * a.blocks + hh / heads;
   // the numbers of its first and last tile, and the CTAs that have them
-  const int64_t s1 = a.prefix[e] * a.mult + (prob + 1) * units - 1, s0 = s1 + 1 - units + kOverhead;
+  const int64_t s1 = start * a.mult + (prob + 1) * units - 1, s0 = s1 + 1 - units + kOverhead;
   int c0 = (int)(s0 * ctas / total), c1 = (int)(s1 * ctas / total);
   while (c0 + 1 < ctas && range_start(total, c0 + 1, ctas) <= s0) ++c0;
   while (c1 + 1 < ctas && range_start(total, c1 + 1, ctas) <= s1) ++c1;
   if (c0 == c1) return;  // written by its CTA
-  const int hrow = hh % heads;
-  __shared__ float sm[kJoinWarps], sl[kJoinWarps];
-  __shared__ float so[kJoinWarps][D];
+  const int hrow = hh % heads, n = c1 - c0 + 1;
+  const auto part = [&](int i) { return (2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0)) * 16 + hrow; };
+  // the parts' weights exp2(m - M), their sum of sums
+  float m = -INFINITY;
+  for (int i = tid; i < n; i += kJoinWarps * 32) {
+    const float y = a.part_ml[part(i)].x;
+    weight[i] = y;
+    m = fmaxf(m, y);
+  }
+  m = warp_max(m);
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
+  float M = red[0][0];
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, red[0][w]);
+  const float base = M == -INFINITY ? 0.f : M;
+  float l = 0.f;
+  for (int i = tid; i < n; i += kJoinWarps * 32) {
+    const float f = exp2f(weight[i] - base);
+    l += a.part_ml[part(i)].y * f;
+    weight[i] = f;
+  }
+  l = warp_sum(l);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  float L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) L += red[1][w];
+  // the outputs: a warp takes every kJoinWarps-th part
   constexpr int V = D / 32;
-  float m = -INFINITY, l = 0.f, o[V];
+  float o[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) o[v] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
-    const int64_t p = (2 * (int64_t)c + (c == c0 ? 1 : 0)) * 16 + hrow;
-    const float2 ml = a.part_ml[p];
-    float x[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = a.part_o[p * D + lane * V + v];
-    const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-    const float f0 = exp2f(m - base), f1 = exp2f(ml.x - base);
-    m = mn;
-    l = l * f0 + ml.y * f1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = o[v] * f0 + x[v] * f1;
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kJoinWarps) {
+    const float f = weight[i];
+    const float* p = a.part_o + part(i) * D + lane * V;
+    if constexpr (V == 4) {
+      const float4 x = *(const float4*)p;
+      o[0] = fmaf(x.x, f, o[0]);
+      o[1] = fmaf(x.y, f, o[1]);
+      o[2] = fmaf(x.z, f, o[2]);
+      o[3] = fmaf(x.w, f, o[3]);
+    } else {
+      const float2 x = *(const float2*)p;
+      o[0] = fmaf(x.x, f, o[0]);
+      o[1] = fmaf(x.y, f, o[1]);
+    }
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) so[warp][lane * V + v] = o[v];
   __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, sm[w]);
-  float f[kJoinWarps];
-  for (int w = 0; w < kJoinWarps; ++w) {
-    f[w] = exp2f(sm[w] - (M == -INFINITY ? 0.f : M));
-    L += sl[w] * f[w];
-  }
-  if (threadIdx.x < D / 2) {
-    const int x = 2 * threadIdx.x;
+  if (tid < D / 2) {
+    const int x = 2 * tid;
     float y0 = 0.f, y1 = 0.f;
+#pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-      y0 += so[w][x] * f[w];
-      y1 += so[w][x + 1] * f[w];
+      y0 += so[w][x];
+      y1 += so[w][x + 1];
     }
     const float inv = kv.v_scale / L;
     *(uint32_t*)(out + x) = L == 0.f ? 0u : pack2<QT>(y0 * inv, y1 * inv);
   }
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     const float y = L == 0.f ? -INFINITY : M + (log2f(L) - bias);
     if (d.lse) d.lse[at] = y * 0.6931471805599453f;
     if (a.lse2) a.lse2[at] = y;
@@ -776,7 +802,7 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttnArgs a) {
   const PagedView& kv = d.kv;
   const int g = blockIdx.y, r = blockIdx.z;
   __shared__ float lse[64];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_wait();
   const Entry n = entry_of(a, r);
   if (threadIdx.x < d.group) {
     const float y = a.lse2[(int64_t)r * d.Hq + g * d.group + threadIdx.x];
@@ -805,8 +831,6 @@ int device_sms() {
   known[dev & 63].store(sms);
   return sms;
 }
-
-constexpr int kMaxSms = 160;  // what the workspace is sized for; a grid is at most kMaxPerSm times it
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -854,15 +878,11 @@ cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
   const int sms = device_sms();
   int64_t grid = (int64_t)per_sm(NB) * (sms < kMaxSms ? sms : kMaxSms);
   if (grid > most) grid = most;
-  if (a.n_entries > kInline) {
-    plan_kernel<<<1, 1024, 0, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_after(attn_kernel<QT, K, D, NB>, dim3((unsigned)grid), kThreads, smem, st, a, km, vm);
-  } else {
-    attn_kernel<QT, K, D, NB><<<(unsigned)grid, kThreads, smem, st>>>(a, km, vm);
-    e = cudaGetLastError();
-  }
-  if (e != cudaSuccess) return e;
+  if (a.n_entries > kInline && (e = launch_after(plan_kernel, dim3(1), 1024, 0, st, a)) != cudaSuccess) return e;
+  // Not launch_after: CTAs of the kernel before it, still waiting on an SM, would keep one of this
+  // kernel's CTAs from fitting there, and the grid is as large as the GPU (332 -> 406 us at 8 x 128K).
+  attn_kernel<QT, K, D, NB><<<(unsigned)grid, kThreads, smem, st>>>(a, km, vm);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const float bias = std::is_same_v<K, __nv_bfloat16> ? 0.f : 15.f;
   e = launch_after(join_kernel<QT, D>, dim3(a.d.Hq, a.d.n_rows), kJoinWarps * 32, 0, st, a, (int)grid, bias);
   if (e != cudaSuccess || !a.logits) return e;

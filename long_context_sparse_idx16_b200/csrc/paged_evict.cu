@@ -7,7 +7,7 @@
 // can stay.
 //
 // pick_kernel: one CTA per (sequence, KV head) reads scores and positions, keeps the keys in shared
-// memory (beyond 48K slots it forms them again in each pass), finds the cut in three radix passes
+// memory (beyond 24K slots it reads them again in each pass), finds the cut in three radix passes
 // and writes the two lists.  move_kernel: the rows, 16 bytes a lane, over the whole GPU; HBM bounds
 // it (each moved row is read and written once).
 #include "paged.cuh"
@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kBins = 2048;
-constexpr int kKeysInSmem = 48 * 1024;
+constexpr int kKeysInSmem = 24 * 1024;
 
 struct PickShared {
   uint32_t hist[kBins];
@@ -48,11 +48,11 @@ __device__ void find_bin(PickShared& s, int want) {
 
 template <bool kSmem>
 __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ uint32_t keys[];  // [n] keys, then [n] positions
   __shared__ PickShared s;
   const PagedView& kv = a.kv;
   const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.launch_dependents;");
+  after_wait();
   const int64_t prob = (int64_t)b * kv.Hkv + g, base = prob * a.stride;
   const float* sc = a.scores + base;
   const int32_t* pos = a.positions + base;
@@ -67,22 +67,33 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
     if (tid == 0) s.newest = INT32_MIN;
     __syncthreads();
     int newest = INT32_MIN;
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) newest = max(newest, pos[i]);
+    int32_t* pos_s = reinterpret_cast<int32_t*>(keys + n);
+    if (kSmem) {
+      // both arrays in one go, scores as they are; then newest is known and the keys are formed
+#pragma unroll 8
+      for (int i = tid; i < n; i += kThreads) {
+        const int p = pos[i];
+        keys[i] = __float_as_uint(sc[i]);
+        pos_s[i] = p;
+        newest = max(newest, p);
+      }
+    } else {
+#pragma unroll 8
+      for (int i = tid; i < n; i += kThreads) newest = max(newest, pos[i]);
+    }
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) atomicMax(&s.newest, newest);
+    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
     __syncthreads();
     const int64_t recent = (int64_t)s.newest - a.n_recent;
+    const auto position = [&](int i) -> int { return kSmem ? pos_s[i] : pos[i]; };
     const auto form = [&](int i) -> uint32_t {
-      const int p = pos[i];
-      const float x = sc[i];
+      const int p = position(i);
+      const float x = kSmem ? __uint_as_float(keys[i]) : sc[i];
       return p < a.n_sink || p > recent ? 0xffffffffu : x != x ? 0u : order_key(x + 0.f);
     };
-    if (kSmem) {
-#pragma unroll 4
-      for (int i = tid; i < n; i += kThreads) keys[i] = form(i);
-    }
-    const auto key = [&](int i) -> uint32_t { return kSmem ? keys[i] : form(i); };
+    bool formed = false;  // each thread forms the keys of its own slots in its first pass over them
+    const auto key = [&](int i) -> uint32_t { return kSmem && formed ? keys[i] : form(i); };
 
     // the cut: digits of 11, 11 and 10 bits; done early when a bin is taken whole
     uint32_t cut = 0;
@@ -91,13 +102,18 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
 #pragma unroll 1
     for (int d = 0; d < 3 && !whole; ++d) {
       const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
-      for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
-      __syncthreads();
+      if (d > 0) {
+        for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+        __syncthreads();
+      }
+#pragma unroll 4
       for (int i = tid; i < n; i += kThreads) {
         const uint32_t x = key(i);
+        if (kSmem && d == 0) keys[i] = x;
         if (d == 0 || (x >> (d == 1 ? 21 : 10)) == (cut >> (d == 1 ? 21 : 10)))
           atomicAdd(&s.hist[d == 2 ? x & 1023u : (x >> shift) & 2047u], 1u);
       }
+      formed = true;
       __syncthreads();
       find_bin(s, want);
       cut |= (uint32_t)s.bin << shift;
@@ -111,13 +127,13 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
       int ties;
       tie_cut = block_kth_largest(n, want, s.small, &ties, [&](int i) -> unsigned long long {
         if (key(i) != cut) return 0ull;
-        return (unsigned long long)~((uint32_t)pos[i] ^ 0x80000000u) << 32 | ~(uint32_t)i;
+        return (unsigned long long)~((uint32_t)position(i) ^ 0x80000000u) << 32 | ~(uint32_t)i;
       });
     }
     const auto stays = [&](int i) -> bool {
       const uint32_t x = key(i);
       if (x != cut || whole) return x >= cut;
-      return ((unsigned long long)~((uint32_t)pos[i] ^ 0x80000000u) << 32 | ~(uint32_t)i) >= tie_cut;
+      return ((unsigned long long)~((uint32_t)position(i) ^ 0x80000000u) << 32 | ~(uint32_t)i) >= tie_cut;
     };
 
     // the lists: a warp takes a contiguous piece, counts, and writes behind the pieces before it
@@ -180,7 +196,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
   const PagedView& kv = a.kv;
   const int g = blockIdx.y, b = blockIdx.z;
   const int64_t prob = (int64_t)b * kv.Hkv + g, base = prob * a.stride;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_wait();
   const int moved = a.n_moves[prob];
   if ((int64_t)blockIdx.x * kMoveRows >= moved) return;
   int seq;
@@ -225,12 +241,12 @@ cudaError_t launch_paged_evict(const EvictArgs& a, cudaStream_t st) {
   cudaError_t e;
   if (cap <= kKeysInSmem) {
     static std::atomic<uint64_t> done{0};
-    if ((e = allow_smem(pick_kernel<true>, kKeysInSmem * sizeof(uint32_t), done)) != cudaSuccess) return e;
-    pick_kernel<true><<<grid, kThreads, cap * sizeof(uint32_t), st>>>(a);
+    if ((e = allow_smem(pick_kernel<true>, kKeysInSmem * 2 * sizeof(uint32_t), done)) != cudaSuccess) return e;
+    e = launch_after(pick_kernel<true>, grid, kThreads, cap * 2 * sizeof(uint32_t), st, a);
   } else {
-    pick_kernel<false><<<grid, kThreads, 0, st>>>(a);
+    e = launch_after(pick_kernel<false>, grid, kThreads, 0, st, a);
   }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (e != cudaSuccess) return e;
   // at most the smaller of the slots kept and the slots dropped move
   const int64_t most = cap - a.budget < a.budget ? cap - a.budget : a.budget;
   if (most <= 0) return cudaSuccess;

@@ -25,39 +25,31 @@ namespace {
 constexpr int kScoreWarps = 8;
 constexpr int kPagesPerWarp = kPageChunk / kScoreWarps;  // 32
 constexpr int kRowBlock = 8;  // rows of a chunk that share one read of the bounds
-constexpr int kMaxM = kRowBlock * 64;  // heads of a run of rows, at most
+constexpr int kMaxM = 64 + 16 * kRowBlock;  // heads of a run of rows that are kept at once
 
 template <typename T>
+using pair_t = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+template <typename T>
+__device__ __forceinline__ pair_t<T> as_pair(uint32_t x) {
+  return *reinterpret_cast<pair_t<T>*>(&x);
+}
+template <typename P>
+__device__ __forceinline__ uint32_t as_bits(P x) {
+  return *reinterpret_cast<uint32_t*>(&x);
+}
+// max(x, 0) and min(x, 0) of a pair; a NaN gives NaN
+template <typename T>
 __device__ __forceinline__ uint32_t pos_part(uint32_t x) {
-  if constexpr (std::is_same_v<T, __half>) {
-    const __half2 y = __hmax2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
-    return *reinterpret_cast<const uint32_t*>(&y);
-  } else {
-    const __nv_bfloat162 y = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&x), __bfloat162bfloat162(__ushort_as_bfloat16(0)));
-    return *reinterpret_cast<const uint32_t*>(&y);
-  }
+  return as_bits(__hmax2_nan(as_pair<T>(x), as_pair<T>(0u)));
 }
 template <typename T>
 __device__ __forceinline__ uint32_t neg_part(uint32_t x) {
-  if constexpr (std::is_same_v<T, __half>) {
-    const __half2 y = __hmin2(*reinterpret_cast<__half2*>(&x), __half2half2(__ushort_as_half(0)));
-    return *reinterpret_cast<const uint32_t*>(&y);
-  } else {
-    const __nv_bfloat162 y = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&x), __bfloat162bfloat162(__ushort_as_bfloat16(0)));
-    return *reinterpret_cast<const uint32_t*>(&y);
-  }
+  return as_bits(__hmin2_nan(as_pair<T>(x), as_pair<T>(0u)));
 }
 // running maximum of magnitudes, in T pairs (NaN shows in the scores themselves)
 template <typename T>
 __device__ __forceinline__ uint32_t abs_max(uint32_t m, uint32_t x) {
-  x &= 0x7fff7fffu;
-  if constexpr (std::is_same_v<T, __half>) {
-    const __half2 y = __hmax2(*reinterpret_cast<__half2*>(&m), *reinterpret_cast<__half2*>(&x));
-    return *reinterpret_cast<const uint32_t*>(&y);
-  } else {
-    const __nv_bfloat162 y = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), *reinterpret_cast<__nv_bfloat162*>(&x));
-    return *reinterpret_cast<const uint32_t*>(&y);
-  }
+  return as_bits(__hmax2(as_pair<T>(m), as_pair<T>(x & 0x7fff7fffu)));
 }
 
 // A run of rows of one sequence inside a block of kRowBlock rows.
@@ -80,108 +72,142 @@ __device__ __forceinline__ Run run_at(const SelectPagesArgs& a, int r, int end) 
 
 // One CTA: a chunk of pages, a KV head, a block of rows.  A warp takes 32 pages, 16 at a time: a lane
 // holds E = 16 bytes' worth of successive dims of page (lane / 4) of an 8-page tile, dims
-// (4 j + lane % 4) E ... of load j, and the query operand is read in the same order, so the
-// contraction needs no shuffling.
+// (4 j + lane % 4) E ... of load j.  The queries lie in shared memory in the order of the
+// contraction that this gives, max(q, 0) and min(q, 0) apart, rows 16 bytes off a multiple of 128.
 template <typename T, typename K, int D>
 __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const SelectPagesArgs a, int row_block, int m_pad) {
   constexpr int E = 16 / (int)sizeof(K);
   constexpr int J = D / (4 * E);  // loads per bound
   constexpr int KS = D / 16;      // steps of 16 terms per bound
-  constexpr int QS = D + 32;      // elements between query rows: 64 bytes off, two rows cover all banks
+  constexpr int QS = 2 * D + 16;  // bytes between query rows
   extern __shared__ __align__(16) uint8_t smem_[];
-  uint16_t* sq = reinterpret_cast<uint16_t*>(smem_);                                // [m_pad][QS]
-  uint32_t* best = reinterpret_cast<uint32_t*>(smem_ + (size_t)m_pad * QS * 2);     // [row_block][kPageChunk]
+  uint8_t* sq = smem_;                                                            // [2][m_pad][QS]
+  uint32_t* best = reinterpret_cast<uint32_t*>(smem_ + (size_t)2 * m_pad * QS);   // [row_block][kPageChunk]
   __shared__ uint32_t s_max;
   const PagedView& kv = a.kv;
   const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r_end = min(a.n_rows, ((int)blockIdx.z + 1) * row_block);
-  asm volatile("griddepcontrol.launch_dependents;");
+  after_wait();
   for (int r = blockIdx.z * row_block; r < r_end;) {
     const Run u = run_at(a, r, r_end);
     r += u.count;
     const int p0 = blockIdx.x * kPageChunk;
     if (p0 >= u.pages) continue;  // the whole CTA alike
-    const int m_rows = u.count * a.group, m_tiles = (m_rows + 15) / 16;
+    const int m_rows = u.count * a.group;
     __syncthreads();
-    for (int i = tid; i < m_tiles * 16 * (D / 8); i += 32 * kScoreWarps) {
-      const int m = i / (D / 8), x = i % (D / 8);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (m < m_rows)
-        v = *(const uint4*)((const T*)a.q + (u.first + m / a.group) * a.q_stride +
-                            (int64_t)(g * a.group + m % a.group) * D + x * 8);
-      *(uint4*)(sq + m * QS + x * 8) = v;
-    }
     for (int i = tid; i < u.count * kPageChunk; i += 32 * kScoreWarps) best[i] = 0u;
     if (tid == 0) s_max = 0u;
-    __syncthreads();
     uint32_t mag = 0u;
-    for (int n0 = 0; n0 < kPagesPerWarp; n0 += 16) {
-      const int pw = p0 + warp * kPagesPerWarp + n0;
-      if (pw >= u.pages) break;
-      // the bounds of two tiles of 8 pages: B operands [tile][hi, lo][step][2]
-      uint32_t bb[2][2][KS][2];
+    // the run's heads, m_pad at a time (all of them, unless groups are large)
+    for (int m0 = 0; m0 < m_rows; m0 += m_pad) {
+      const int m_n = min(m_rows - m0, m_pad), m_tiles = (m_n + 15) / 16;
+      __syncthreads();
+      for (int i = tid; i < m_tiles * 16 * (D / 4); i += 32 * kScoreWarps) {
+        // four dims: lane c's share of step k, two slots at 2 c and two at 8 + 2 c
+        const int m = i / (D / 4), d = i % (D / 4) * 4, c = d / E % 4, k = d / (4 * E) * (E / 4) + d % E / 4;
+        uint2 v = make_uint2(0u, 0u);
+        if (m < m_n)
+          v = *(const uint2*)((const T*)a.q + (u.first + (m0 + m) / a.group) * a.q_stride +
+                              (int64_t)(g * a.group + (m0 + m) % a.group) * D + d);
+        uint8_t* at = sq + m * QS + k * 32 + c * 4;
+        *(uint32_t*)at = pos_part<T>(v.x);
+        *(uint32_t*)(at + 16) = pos_part<T>(v.y);
+        *(uint32_t*)(at + m_pad * QS) = neg_part<T>(v.x);
+        *(uint32_t*)(at + m_pad * QS + 16) = neg_part<T>(v.y);
+      }
+      __syncthreads();
+      for (int n0 = 0; n0 < kPagesPerWarp; n0 += 16) {
+        const int pw = p0 + warp * kPagesPerWarp + n0;
+        if (pw >= u.pages) break;
+        // the bounds of two tiles of 8 pages: B operands [tile][hi, lo][step][2]
+        uint32_t bb[2][2][KS][2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int p = pw + t * 8 + (lane >> 2);
-        const int64_t page = p < u.pages ? paged_page(kv, u.seq, p) : -1;
-        const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * D + (lane & 3) * E;
-        if (p < u.pages && page < 0 && (lane & 3) == 0)  // no number: the exact path ranks it last
-          for (int i = 0; i < u.count; ++i) atomicMax(&best[i * kPageChunk + p - p0], 0xffffffffu);
+        for (int t = 0; t < 2; ++t) {
+          const int p = pw + t * 8 + (lane >> 2);
+          const int64_t page = p < u.pages ? paged_page(kv, u.seq, p) : -1;
+          const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * D + (lane & 3) * E;
+          if (p < u.pages && page < 0 && (lane & 3) == 0)  // no number: the exact path ranks it last
+            for (int i = 0; i < u.count; ++i) atomicMax(&best[i * kPageChunk + p - p0], 0xffffffffu);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int j = 0; j < J; ++j) {
-            const uint4 v = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : ld_nc_u4(lim + (x ? 0 : D) + j * 4 * E);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int j = 0; j < J; ++j) {
+              const uint4 v = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : ld_nc_u4(lim + (x ? 0 : D) + j * 4 * E);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (sizeof(K) == 1) {
-                bb[t][x][4 * j + e][0] = widen2<T>(w[e]);
-                bb[t][x][4 * j + e][1] = widen2<T>(w[e] >> 16);
-              } else {
-                bb[t][x][2 * j + (e >> 1)][e & 1] = w[e];
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (sizeof(K) == 1) {
+                  bb[t][x][4 * j + e][0] = widen2<T>(w[e]);
+                  bb[t][x][4 * j + e][1] = widen2<T>(w[e] >> 16);
+                } else {
+                  bb[t][x][2 * j + (e >> 1)][e & 1] = w[e];
+                }
               }
             }
+        }
+        if (m0 == 0) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int k = 0; k < KS; ++k) mag = abs_max<T>(abs_max<T>(mag, bb[t][x][k][0]), bb[t][x][k][1]);
+        }
+        __syncwarp();
+        uint32_t* out = best + warp * kPagesPerWarp + n0;  // [row][page of this warp's 16]
+#pragma unroll 1
+        for (int mt = 0; mt < m_tiles; ++mt) {
+          float c[2][4] = {};
+          const uint32_t at = smem_u32(sq + (mt * 16 + (lane & 15)) * QS + (lane >> 4) * 16);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            uint32_t f[4];
+            ldsm_x4(at + k * 32, f[0], f[1], f[2], f[3]);
+            mma<T>(c[0], f, bb[0][0][k][0], bb[0][0][k][1]);
+            mma<T>(c[1], f, bb[1][0][k][0], bb[1][0][k][1]);
+            ldsm_x4(at + m_pad * QS + k * 32, f[0], f[1], f[2], f[3]);
+            mma<T>(c[0], f, bb[0][1][k][0], bb[0][1][k][1]);
+            mma<T>(c[1], f, bb[1][1][k][0], bb[1][1][k][1]);
           }
+          // the greatest head of each row, as order keys (a NaN of the products is the greatest key).
+          // c[t][e]: head lane / 4 + 8 (e / 2), page 8 t + 2 (lane % 4) + e % 2
+          const int m = m0 + mt * 16 + (lane >> 2);
+          if ((a.group & 7) == 0) {
+            // eight heads of a row in the eight lanes of a page: halved three times, each lane ends
+            // with one of the eight (row half, tile, page parity) combinations
+            uint32_t key[8];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 8; ++x) key[x] = order_key(c[(x >> 1) & 1][(x & 1) + (x >> 2) * 2]);
+            const int hi2 = (lane >> 4) & 1, hi1 = (lane >> 3) & 1, hi0 = (lane >> 2) & 1;
 #pragma unroll
-          for (int k = 0; k < KS; ++k) mag = abs_max<T>(abs_max<T>(mag, bb[t][x][k][0]), bb[t][x][k][1]);
-      }
-      for (int mt = 0; mt < m_tiles; ++mt) {
-        float c[2][4] = {};
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t mine = hi2 ? key[x + 4] : key[x], other = hi2 ? key[x] : key[x + 4];
+              key[x] = max(mine, __shfl_xor_sync(0xffffffffu, other, 16));
+            }
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          // terms of step k: dims of this lane (4 of E successive ones)
-          const int dim = sizeof(K) == 1 ? ((k >> 2) * 4 + (lane & 3)) * E + (k & 3) * 4
-                                         : ((k >> 1) * 4 + (lane & 3)) * E + (k & 1) * 4;
-          const uint2 q0 = *(const uint2*)(sq + (mt * 16 + (lane >> 2)) * QS + dim);
-          const uint2 q1 = *(const uint2*)(sq + (mt * 16 + 8 + (lane >> 2)) * QS + dim);
-          const uint32_t ap[4] = {pos_part<T>(q0.x), pos_part<T>(q1.x), pos_part<T>(q0.y), pos_part<T>(q1.y)};
-          const uint32_t an[4] = {neg_part<T>(q0.x), neg_part<T>(q1.x), neg_part<T>(q0.y), neg_part<T>(q1.y)};
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t mine = hi1 ? key[x + 2] : key[x], other = hi1 ? key[x] : key[x + 2];
+              key[x] = max(mine, __shfl_xor_sync(0xffffffffu, other, 8));
+            }
+            const uint32_t mine = hi0 ? key[1] : key[0], other = hi0 ? key[0] : key[1];
+            const uint32_t top = max(mine, __shfl_xor_sync(0xffffffffu, other, 4));
+            const int row = m0 + mt * 16 + hi2 * 8;
+            if (row < m_rows) {
+              uint32_t* to = out + row / a.group * kPageChunk + hi1 * 8 + (lane & 3) * 2 + hi0;
+              if (a.group == 8) *to = max(*to, top);  // nobody else writes it now
+              else atomicMax(to, top);
+            }
+          } else {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            mma<T>(c[t], ap, bb[t][0][k][0], bb[t][0][k][1]);
-            mma<T>(c[t], an, bb[t][1][k][0], bb[t][1][k][1]);
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int x = m + (e >> 1) * 8;
+                if (x < m_rows)
+                  atomicMax(out + x / a.group * kPageChunk + t * 8 + (lane & 3) * 2 + (e & 1), order_key(c[t][e]));
+              }
           }
         }
-        // the greatest head of each row: through shared memory, as order keys (NaN above all others);
-        // eight heads of one row are joined in registers first where groups are whole eights
-        const bool eights = (a.group & 7) == 0;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = mt * 16 + (lane >> 2) + (e >> 1) * 8;
-            uint32_t key = m >= m_rows ? 0u : c[t][e] != c[t][e] ? 0xffffffffu : order_key(c[t][e]);
-            if (eights) {
-              key = max(key, __shfl_xor_sync(0xffffffffu, key, 4));
-              key = max(key, __shfl_xor_sync(0xffffffffu, key, 8));
-              key = max(key, __shfl_xor_sync(0xffffffffu, key, 16));
-            }
-            if (m < m_rows && (!eights || lane < 4))
-              atomicMax(&best[m / a.group * kPageChunk + warp * kPagesPerWarp + n0 + t * 8 + (lane & 3) * 2 + (e & 1)], key);
-          }
       }
     }
     // magnitude of the bounds seen
@@ -214,29 +240,12 @@ constexpr int kPagesInSmem = 48 * 1024;
 struct PickShared {
   uint32_t hist[kBins];
   uint32_t small[257];
-  float fa[32], fb[32];
+  float f[4][32];
   int sums[33];
-  int bin, above, n_between, n_in;
-  float lo, hi;
+  int bin, n_in, n_between, got;
   int idx[kMaxBetween];
   unsigned long long key[kMaxBetween];
 };
-
-template <int kT>
-__device__ __forceinline__ float block_extreme(float x, bool want_max, float* sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float y = __shfl_xor_sync(0xffffffffu, x, o);
-    x = want_max ? fmaxf(x, y) : fminf(x, y);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = sh[0];
-#pragma unroll
-  for (int w = 1; w < kT / 32; ++w) x = want_max ? fmaxf(x, sh[w]) : fminf(x, sh[w]);
-  return x;
-}
 
 // Exact key of a page, by one warp; 0 (last) for a page outside the pool or a score that is no number.
 template <typename T, typename K>
@@ -280,6 +289,9 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
   __shared__ PickShared s;
   const PagedView& kv = a.kv;
   const int g = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kBins; i += kT) s.hist[i] = 0;
+  if (tid == 0) s.got = 0;
+  after_wait();
   int seq;
   const int len = paged_row(kv, a.row_seq, a.row_len, r, &seq);
   if (g == 0 && tid == 0 && paged_row_bad(kv, a.row_seq, a.row_len, r)) paged_err(kv, RTP_PAGED_ERANGE);
@@ -294,17 +306,20 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
   float* ws = a.approx + prob * kv.max_pages;
   float* x = kSmem ? list_ : ws;
   const T* q = (const T*)a.q + r * a.q_stride + (int64_t)g * a.group * kv.D;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  float cut = INFINITY;  // pages above it are in
+  // a page is in if its score lies in a bin from `cut` on, or is +inf
+  float lo = 0.f, scale = 0.f;
+  int cut = kBins;
+  const auto bin_of = [&](float y) { return min(kBins - 1, (int)((y - lo) * scale)); };
   if (want > 0 && want < c1 - c0) {
     // the scores' range; eps
-    float lo = INFINITY, hi = -INFINITY, mag = 0.f, q1 = 0.f;
+    float low = INFINITY, high = -INFINITY, mag = 0.f, q1 = 0.f;
     bool odd = false;
+#pragma unroll 4
     for (int i = c0 + tid; i < c1; i += kT) {
       const float y = ws[i];
       if (kSmem) x[i] = y;
-      lo = fminf(lo, y);
-      hi = fmaxf(hi, y);
+      low = fminf(low, y);
+      high = fmaxf(high, y);
       odd |= !isfinite(y);
     }
     for (int i = tid; i < chunks && i * kPageChunk < pages; i += kT) mag = fmaxf(mag, a.chunk_max[prob * chunks + i]);
@@ -313,79 +328,64 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
       for (int d = lane; d < kv.D; d += 32) y += fabsf(to_f32(q[u * kv.D + d]));
       q1 = fmaxf(q1, warp_sum(y));
     }
-    lo = block_extreme<kT>(lo, false, s.fa);
-    hi = block_extreme<kT>(hi, true, s.fb);
-    mag = block_extreme<kT>(mag, true, s.fa);
-    q1 = block_extreme<kT>(q1, true, s.fb);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+      high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+      mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, o));
+    }
+    if (lane == 0) {
+      s.f[0][warp] = low;
+      s.f[1][warp] = high;
+      s.f[2][warp] = mag;
+      s.f[3][warp] = q1;
+    }
+    odd = __syncthreads_or(odd);
+#pragma unroll
+    for (int w = 0; w < kT / 32; ++w) {
+      low = fminf(low, s.f[0][w]);
+      high = fmaxf(high, s.f[1][w]);
+      mag = fmaxf(mag, s.f[2][w]);
+      q1 = fmaxf(q1, s.f[3][w]);
+    }
     // 1.01 covers the rounding of |q|_1 and of this product; 2^-110 what underflows in fp32
     const float eps = 1.01f * 6.103515625e-05f * q1 * mag + 7.7e-34f;
-    odd = __syncthreads_or(odd || !isfinite(eps));
-    bool done = false;
-    float cut_lo = -INFINITY;
-    for (int round = 0; round < 4 && !odd && !done; ++round) {
-      // histogram of [lo, hi]; the page wanted last lies in it
-      for (int i = tid; i < kBins; i += kT) s.hist[i] = 0;
-      if (tid == 0) s.n_between = s.n_in = 0;
+    // Bins at least 2.5 eps wide (a bin's place is off by less than 2^-12 of a bin): whatever lies
+    // within 2 eps of the last page taken lies in its bin or a neighbouring one.
+    const float range = high - low;
+    bool done = !odd && isfinite(eps) && isfinite(range);
+    if (done) {
+      lo = low;
+      scale = fminf((float)kBins / fmaxf(range, 1e-30f), 0.4f / eps);
+      for (int i = c0 + tid; i < c1; i += kT) atomicAdd(&s.hist[bin_of(x[i])], 1u);
       __syncthreads();
-      const float scale = hi > lo ? kBins / (hi - lo) : 0.f;
-      const auto bin_of = [&](float y) { return min(kBins - 1, (int)((y - lo) * scale)); };
-      int above = 0;
-      for (int i = c0 + tid; i < c1; i += kT) {
-        const float y = x[i];
-        if (y > hi) ++above;
-        else if (y >= lo) atomicAdd(&s.hist[bin_of(y)], 1u);
-      }
-      above = __reduce_add_sync(0xffffffffu, above);
-      if (lane == 0 && above) atomicAdd(&s.n_in, above);
-      __syncthreads();
-      above = s.n_in;
       constexpr int B = kBins / kT;
       int c[B], sum = 0, total;
 #pragma unroll
       for (int e = 0; e < B; ++e) sum += c[e] = (int)s.hist[kBins - 1 - (tid * B + e)];
-      int before = above + block_exclusive(sum, s.sums, &total);
+      int before = block_exclusive(sum, s.sums, &total);
 #pragma unroll
       for (int e = 0; e < B; ++e) {
-        if (before < want && before + c[e] >= want) s.bin = kBins - 1 - (tid * B + e);
+        if (before < want && before + c[e] >= want) {
+          const int bin = kBins - 1 - (tid * B + e);
+          const int up = bin + 1 < kBins ? (int)s.hist[bin + 1] : 0, down = bin > 0 ? (int)s.hist[bin - 1] : 0;
+          s.bin = bin;
+          s.n_in = before - up;
+          s.n_between = up + c[e] + down;
+        }
         before += c[e];
       }
-      if (tid == 0) s.n_in = 0;
-      __syncthreads();
-      const int bin = s.bin;
-      // the bin's own range, then everything within 2 eps of it
-      float blo = INFINITY, bhi = -INFINITY;
-      for (int i = c0 + tid; i < c1; i += kT) {
-        const float y = x[i];
-        if (y >= lo && y <= hi && bin_of(y) == bin) {
-          blo = fminf(blo, y);
-          bhi = fmaxf(bhi, y);
-        }
-      }
-      blo = block_extreme<kT>(blo, false, s.fa);
-      bhi = block_extreme<kT>(bhi, true, s.fb);
-      cut = __fadd_ru(bhi, 2.f * eps);
-      cut_lo = __fadd_rd(blo, -2.f * eps);
-      int in = 0;
-      for (int i = c0 + tid; i < c1; i += kT) {
-        const float y = x[i];
-        if (y > cut) {
-          ++in;
-        } else if (y >= cut_lo) {
-          const int at = atomicAdd(&s.n_between, 1);
-          if (at < kMaxBetween) s.idx[at] = i;
-        }
-      }
-      in = __reduce_add_sync(0xffffffffu, in);
-      if (lane == 0 && in) atomicAdd(&s.n_in, in);
       __syncthreads();
       done = s.n_between <= kMaxBetween;
-      if (!done && bhi - blo <= 4.f * eps) break;  // a finer histogram would not help
-      lo = blo;
-      hi = bhi;
-      __syncthreads();
     }
     if (done) {
-      const int m = s.n_between, need = want - s.n_in;
+      const int bin = s.bin, m = s.n_between, need = want - s.n_in;
+      cut = bin + 2;
+      for (int i = c0 + tid; i < c1; i += kT) {
+        const int b = bin_of(x[i]);
+        if (b >= bin - 1 && b <= bin + 1) s.idx[atomicAdd(&s.got, 1)] = i;
+      }
+      __syncthreads();
       for (int j = warp; j < m; j += kT / 32) {
         const unsigned long long k = exact_key<T, K>(a, q, seq, g, s.idx[j]);
         if (lane == 0) s.key[j] = k;
@@ -396,9 +396,8 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
         const int i = s.idx[j];
         int rank = 0;
         for (int l = 0; l < m; ++l) rank += s.key[l] > k || (s.key[l] == k && s.idx[l] < i);
-        x[i] = rank < need ? INFINITY : -INFINITY;
+        x[i] = rank < need ? INFINITY : lo;  // lo lies in bin 0, below the cut
       }
-      if (cut == INFINITY) cut = 3.402823466e+38f;  // an overflowed sum: the chosen still lie above
       __syncthreads();
     } else {
       // every page by its exact score
@@ -417,10 +416,11 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
         const bool eq = i < c1 && k == kth;
         int total;
         const int e = block_exclusive(eq, s.sums, &total);
-        if (i < c1) x[i] = k > kth || (eq && tied + e < ties) ? INFINITY : -INFINITY;
+        if (i < c1) x[i] = k > kth || (eq && tied + e < ties) ? INFINITY : 0.f;
         tied += total;
       }
-      cut = 0.f;
+      lo = scale = 0.f;
+      cut = kBins;
       __syncthreads();
     }
   }
@@ -428,7 +428,12 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
   const bool all = want >= c1 - c0;
   const int per = (pages + kT - 1) / kT * 32;
   const int i0 = warp * per, i1 = min(pages, i0 + per);
-  const auto taken = [&](int i) { return i < c0 || i >= c1 || all || (want > 0 && x[i] > cut); };
+  const auto taken = [&](int i) {
+    if (i < c0 || i >= c1 || all) return true;
+    if (want <= 0) return false;
+    const float y = x[i];
+    return y == INFINITY || bin_of(y) >= cut;
+  };
   int n = 0;
   for (int i = i0 + lane; i - lane < i1; i += 32) n += __popc(__ballot_sync(0xffffffffu, i < i1 && taken(i)));
   int total;
@@ -456,17 +461,21 @@ template <typename T, typename K, int D>
 cudaError_t run_select(const SelectPagesArgs& a, cudaStream_t st) {
   const int chunks = page_chunks(a.kv.max_pages);
   const int row_block = a.row_seq ? kRowBlock : 1;
-  const int m_pad = (row_block * a.group + 15) / 16 * 16;
-  const size_t smem = (size_t)m_pad * (D + 32) * 2 + (size_t)row_block * kPageChunk * sizeof(uint32_t);
+  int m_pad = (row_block * a.group + 15) / 16 * 16;
+  if (m_pad > kMaxM) m_pad = kMaxM;
+  constexpr int QS = 2 * D + 16;
+  const size_t smem = (size_t)2 * m_pad * QS + (size_t)row_block * kPageChunk * sizeof(uint32_t);
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(page_score_kernel<T, K, D>,
-                             (size_t)kMaxM * (D + 32) * 2 + kRowBlock * kPageChunk * sizeof(uint32_t), done);
+  cudaError_t e = allow_smem(page_score_kernel<T, K, D>, (size_t)2 * kMaxM * QS + kRowBlock * kPageChunk * sizeof(uint32_t),
+                             done);
   if (e != cudaSuccess) return e;
-  page_score_kernel<T, K, D><<<dim3(chunks, a.kv.Hkv, (a.n_rows + row_block - 1) / row_block), 32 * kScoreWarps, smem, st>>>(
-      a, row_block, m_pad);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // long lists want more threads for their passes, short ones more CTAs at once
-  return a.kv.max_pages > 2048 ? run_pick<T, K, 1024>(a, chunks, st) : run_pick<T, K, 256>(a, chunks, st);
+  e = launch_after(page_score_kernel<T, K, D>, dim3(chunks, a.kv.Hkv, (a.n_rows + row_block - 1) / row_block),
+                   32 * kScoreWarps, smem, st, a, row_block, m_pad);
+  if (e != cudaSuccess) return e;
+  // Few lists: as many threads as a CTA has, for the latency; many: small CTAs, many at once.
+  const int64_t lists = (int64_t)a.n_rows * a.kv.Hkv;
+  if (lists <= 2 * 148 || a.kv.max_pages > 8192) return run_pick<T, K, 1024>(a, chunks, st);
+  return run_pick<T, K, 128>(a, chunks, st);
 }
 
 template <typename T, typename K>
