@@ -34,12 +34,14 @@ struct PagedView {
   uint32_t* err;
 };
 
-// Every kernel of these operators is launched so that it may start while the one before it drains
-// (launch_after), and calls this before it touches global memory: it lets the next one start and
-// waits until the one before has finished.
+// A kernel launched by launch_after may start while the one before it drains, and waits here until
+// that one has finished and its writes can be seen.  Only then does it let the next one start: when
+// a kernel starts, all work before its predecessor is done, so the second and later kernels of an
+// operator may read the operator's inputs before they wait (but nothing that the predecessor
+// writes).  The first kernel of an operator waits before it touches global memory.
 __device__ __forceinline__ void after_wait() {
-  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
 }
 
 __device__ __forceinline__ void paged_err(const PagedView& p, uint32_t bit) {

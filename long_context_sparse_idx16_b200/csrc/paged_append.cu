@@ -161,15 +161,21 @@ struct Range8 {
   }
 };
 
-// Sequence of token t: the last b with cu[b] <= t.
+// Sequence of token t: the last b with cu[b] <= t, or -1 behind the last sequence.  A warp looks at
+// 32 places at a time.
 __device__ __forceinline__ int token_seq(const int32_t* cu, int n_seqs, int t) {
-  int lo = 0, hi = n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu[mid] <= t) lo = mid;
-    else hi = mid - 1;
+  int lo = 0, n = n_seqs + 1;  // the answer lies in [lo, lo + n)
+  while (n > 32) {
+    const int step = (n + 31) / 32, at = lo + (threadIdx.x & 31) * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, at <= n_seqs && cu[min(at, n_seqs)] <= t);
+    const int k = 31 - __clz(le | 1u);
+    n = min(step, lo + n - (lo + k * step));
+    lo += k * step;
   }
-  return lo;
+  const int at = lo + (threadIdx.x & 31);
+  const uint32_t le = __ballot_sync(0xffffffffu, (threadIdx.x & 31) < n && cu[min(at, n_seqs)] <= t);
+  const int b = lo + 31 - __clz(le | 1u);
+  return b < n_seqs ? b : -1;
 }
 
 // Row groups of a token: ceil(Hq / R) of q, then ceil(Hkv / R) of k, then as many of v; `run` of them
@@ -186,8 +192,8 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
   if (t >= a.n_tokens) return;
   int b = t, i = 0;
   if (a.cu_new) {
-    if (t >= a.cu_new[kv.n_seqs]) return;  // rows behind the last sequence stay as they are
     b = token_seq(a.cu_new, kv.n_seqs, t);
+    if (b < 0) return;  // rows behind the last sequence stay as they are
     i = t - a.cu_new[b];
   }
   const int gq = (a.Hq + R - 1) / R, gk = (kv.Hkv + R - 1) / R;
@@ -326,8 +332,8 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
 }
 
 // Bounds of page `i` of sequence b for KV head g over slots [first, last) of it: lanes hold eight
-// dims each, the CTA's row groups take every R-th slot.  `widen`: from the stored bounds on, unless
-// slot 0 is among them.
+// dims each, the CTA's row groups take every R-th slot.  `widen` (behind the append kernel): from the
+// stored bounds on, unless slot 0 is among them.
 constexpr int kBoundThreads = 128;
 
 template <typename K, int D>
@@ -338,6 +344,7 @@ __device__ void bounds_of(const PagedView& kv, int b, int i, int g, int first, i
   using Raw = typename Pack8<K>::type;
   const int c = (threadIdx.x % L) * 8, r = threadIdx.x / L;
   const int64_t page = paged_page(kv, b, i);
+  if (widen) after_wait();
   if (page < 0) {
     if (threadIdx.x == 0) paged_err(kv, RTP_PAGED_ERANGE);
     return;
@@ -368,14 +375,13 @@ __global__ void __launch_bounds__(kBoundThreads) append_bounds_kernel(const Appe
   __shared__ uint32_t sh[kBoundThreads * 8 / D][2][D / 2];
   const PagedView& kv = a.kv;
   const int b = blockIdx.z;
-  after_wait();
+  // (the lengths and the table are inputs of the whole operator: read ahead)
   const int n = a.cu_new[b + 1] - a.cu_new[b];
   const int64_t cap = (int64_t)kv.max_pages << kv.page_shift;
   const int64_t s0 = a.seq_len[b], s1 = min(s0 + n, cap);
-  if (s0 < 0) return;
   const int64_t i = (s0 >> kv.page_shift) + blockIdx.x;
   const int64_t first = max(s0, i << kv.page_shift), last = min(s1, (i + 1) << kv.page_shift);
-  if (first >= last) return;
+  if (s0 < 0 || first >= last) return after_wait();
   const int64_t base = i << kv.page_shift;
   bounds_of<K, D>(kv, b, (int)i, blockIdx.y, (int)(first - base), (int)(last - base), true, sh);
 }

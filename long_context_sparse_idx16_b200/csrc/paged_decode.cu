@@ -63,6 +63,8 @@ struct AttnArgs {
   float* lse2;           // [rows][Hq] base-2 log-sum-exp, or NULL
   float* logits;         // [rows][Hq][cap] base-2 scores, or NULL
   int64_t cap;
+  int4* split;           // [CTAs] problem that the CTA begins and others go on with: (row, query head,
+                         // heads, last CTA), or row -1
   float2* part_ml;       // [CTAs][continued, begun][16]
   float* part_o;         // [CTAs][continued, begun][16][D]
 };
@@ -158,16 +160,21 @@ __device__ __forceinline__ void tile_prefix(const AttnArgs& a, int64_t* out, int
   if (lane == 0) out[a.n_entries] = run;
 }
 
-// More entries than kInline: one CTA writes the prefix for everybody.
+// More entries than kInline: one CTA writes the prefix for everybody, kPlan entries a thread at a time.
+constexpr int kPlan = 4;
 __global__ void __launch_bounds__(1024) plan_kernel(const AttnArgs a) {
-  __shared__ int64_t sums[32];
+  __shared__ int64_t sums[33];
   after_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t run = 0;
-  for (int e0 = 0; e0 < a.n_entries; e0 += 1024) {
-    const int e = e0 + tid;
-    const int64_t t = e < a.n_entries ? units_of(entry_of(a, e)) : 0;
-    int64_t y = t;
+  for (int e0 = 0; e0 < a.n_entries; e0 += 1024 * kPlan) {
+    const int e = e0 + tid * kPlan;
+    int64_t t[kPlan], own = 0;
+#pragma unroll
+    for (int u = 0; u < kPlan; ++u) t[u] = e + u < a.n_entries ? units_of(entry_of(a, e + u)) : 0;
+#pragma unroll
+    for (int u = 0; u < kPlan; ++u) own += t[u];
+    int64_t y = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
@@ -175,13 +182,25 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnArgs a) {
     }
     if (lane == 31) sums[warp] = y;
     __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += sums[w];
-      all += sums[w];
+    if (warp == 0) {
+      const int64_t w = sums[lane];
+      int64_t x = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t z = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += z;
+      }
+      sums[lane] = x - w;
+      if (lane == 31) sums[32] = x;
     }
-    if (e < a.n_entries) a.prefix[e] = run + before + y - t;
-    run += all;
+    __syncthreads();
+    int64_t at = run + sums[warp] + y - own;
+#pragma unroll
+    for (int u = 0; u < kPlan; ++u) {
+      if (e + u < a.n_entries) a.prefix[e + u] = at;
+      at += t[u];
+    }
+    run += sums[32];
     __syncthreads();
   }
   if (tid == 0) a.prefix[a.n_entries] = run;
@@ -291,10 +310,22 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
   }
   __syncthreads();
   const int64_t* prefix = inl ? sh.prefix : a.prefix;
-  if (inl && blockIdx.x == 0)
-    for (int e = tid; e <= a.n_entries; e += kThreads) a.prefix[e] = sh.prefix[e];
   const int64_t total = prefix[a.n_entries] * a.mult;
   const int ctas = (int)min((int64_t)gridDim.x, total);
+  if (tid == 32 * kConsumers) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);  // the thread that may overwrite it
+  // entries without a tile: zeros
+  for (int e = blockIdx.x; e < a.n_entries; e += gridDim.x) {
+    const int r = d.sel ? e / kv.Hkv : e;
+    if (tid == 0 && paged_row_bad(kv, d.row_seq, d.row_len, r)) paged_err(kv, RTP_PAGED_ERANGE);
+    if (prefix[e + 1] != prefix[e]) continue;
+    const int h = d.sel ? e % kv.Hkv * d.group : 0, nh = d.sel ? d.group : d.Hq;
+    uint16_t* out = (uint16_t*)d.out + r * d.out_stride + (int64_t)h * D;
+    for (int x = tid; x < nh * D / 8; x += kThreads) ((uint4*)out)[x] = make_uint4(0u, 0u, 0u, 0u);
+    for (int x = tid; x < nh; x += kThreads) {
+      if (d.lse) d.lse[(int64_t)r * d.Hq + h + x] = -INFINITY;
+      if (a.lse2) a.lse2[(int64_t)r * d.Hq + h + x] = -INFINITY;
+    }
+  }
   if ((int)blockIdx.x >= ctas) return;
   const int64_t t0 = range_start(total, blockIdx.x, ctas), t1 = range_start(total, blockIdx.x + 1, ctas);
 
@@ -305,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
     const bool mine = is_v < 2;
     const CUtensorMap* map = is_v ? &vm : &km;
     const uint32_t dst0 = ring + is_v * S::kHalf + blk * (kTile * 128) + bi * a.box * S::kRow;
-    const int subs = kv.page_size / a.box;
+    const int sub_shift = kv.page_size > kTile ? 1 : 0;  // boxes per page: 1 or 2
     bool dead = false;
     int st = 0;
     uint32_t phase = 0, jphase = 0;
@@ -333,34 +364,52 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
         j.whole = s.count == s.n.tiles;
         j.last = t >= t1;
         mbar_expect_tx(job_full, s.count ? nh * 2 * D : 0);
+        if (s.count && s.first == 0 && s.count < s.n.tiles) {
+          // the CTA with the problem's last tile
+          const int64_t end = t + (s.n.tiles - s.count) - 1;
+          int c1 = (int)(end * ctas / total);
+          while (c1 + 1 < ctas && range_start(total, c1 + 1, ctas) <= end) ++c1;
+          a.split[blockIdx.x] = make_int4(s.n.row, g * d.group + h0, nh, c1);
+        }
       }
       __syncwarp();
       if (lane < nh && s.count)
         bulk_load(smem_u32(sh.q[lane]),
                   (const uint16_t*)d.q + s.n.row * d.q_stride + (int64_t)(g * d.group + h0 + lane) * D, 2 * D, job_full);
       jphase ^= 1u;
-      for (int i = s.first; i < s.first + s.count; ++i) {
-        int base = kNoSlot, page = 0;  // the box's first slot
-        if (mine) {
-          if (d.sel) {
-            const int64_t b = (int64_t)i * boxes + bi;
-            const int64_t li = b / subs;
-            if (li < s.n.n_list) {
-              const int p = s.n.list[li];
-              if (p >= 0 && p < kv.max_pages) base = (p << kv.page_shift) + (int)(b % subs) * a.box;
-            }
-          } else {
-            base = (i < s.n.t_sink ? i : i + s.n.t_skip) * kTile + bi * a.box;
-          }
-          if (base >= s.n.len || (base + a.box <= s.n.lo && base >= s.n.sinks)) {
-            base = kNoSlot;
-          } else {
-            page = (int)paged_page(kv, s.n.seq, base >> kv.page_shift);
-            if (page < 0) {
-              paged_err(kv, RTP_PAGED_ERANGE);
-              base = kNoSlot;
-            }
-          }
+      // One tile ahead in the page table, two in the list: the look-ups' latency passes while the
+      // ring is full.
+      const int end = s.first + s.count;
+      const auto listed = [&](int i) -> int {  // the list's entry for this lane's box of tile i
+        const int64_t li = ((int64_t)i * boxes + bi) >> sub_shift;
+        return mine && i < end && li < s.n.n_list ? s.n.list[li] : -1;
+      };
+      const auto slot_of = [&](int i, int p) -> int {  // the box's first slot
+        if (!mine || i >= end) return kNoSlot;
+        int base;
+        if (d.sel) {
+          if (p < 0 || p >= kv.max_pages) return kNoSlot;
+          base = (p << kv.page_shift) + (((i * boxes + bi) & sub_shift) ? a.box : 0);
+        } else {
+          base = (i < s.n.t_sink ? i : i + s.n.t_skip) * kTile + bi * a.box;
+        }
+        return base >= s.n.len || (base + a.box <= s.n.lo && base >= s.n.sinks) ? kNoSlot : base;
+      };
+      const auto page_of = [&](int base) -> int {
+        return base == kNoSlot ? 0 : kv.table[(int64_t)s.n.seq * kv.table_stride + (base >> kv.page_shift)];
+      };
+      int next_base = slot_of(s.first, d.sel ? listed(s.first) : 0);
+      int next_page = page_of(next_base);
+      int next_list = d.sel ? listed(s.first + 1) : 0;
+      for (int i = s.first; i < end; ++i) {
+        int base = next_base;
+        const int page = next_page;
+        next_base = slot_of(i + 1, next_list);
+        next_page = page_of(next_base);
+        if (d.sel) next_list = listed(i + 2);
+        if (base != kNoSlot && (uint32_t)page >= (uint64_t)kv.n_pages) {
+          paged_err(kv, RTP_PAGED_ERANGE);
+          base = kNoSlot;
         }
         const bool load = base != kNoSlot;
         dead = !mbar_wait(empty + 8 * st, phase ^ 1u) || *stop;
@@ -689,44 +738,24 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
   }
 }
 
-// One CTA per (query head, row): the partial results of a problem that crosses CTAs, in CTA order;
-// zeros for a row without slots.
+// One CTA per (CTA of attn_kernel, query head of a problem): the partial results of the problem that
+// the CTA begins and others go on with, in CTA order.
 constexpr int kJoinWarps = 8;
 
 template <typename QT, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a, int grid, float bias) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a, float bias) {
   const DecodeArgs& d = a.d;
   const PagedView& kv = d.kv;
-  const int h = blockIdx.x, r = blockIdx.y, g = h / d.group, hh = h % d.group;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int e = d.sel ? r * kv.Hkv + g : r;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c0 = blockIdx.x, hrow = blockIdx.y;
   __shared__ float weight[kMaxPerSm * kMaxSms];
   __shared__ float red[2][kJoinWarps];
   __shared__ float so[kJoinWarps][D];
   after_wait();
-  if (h == 0 && tid == 0 && paged_row_bad(kv, d.row_seq, d.row_len, r)) paged_err(kv, RTP_PAGED_ERANGE);
-  const int64_t start = a.prefix[e], units = a.prefix[e + 1] - start, all = a.prefix[a.n_entries];
+  const int4 s = a.split[c0];
+  if (s.x < 0 || hrow >= s.z) return;
+  const int r = s.x, h = s.y + hrow, n = s.w - c0 + 1;
   uint16_t* out = (uint16_t*)d.out + r * d.out_stride + (int64_t)h * D;
   const int64_t at = (int64_t)r * d.Hq + h;
-  if (units == 0) {
-    if (tid < D / 2) *(uint32_t*)(out + 2 * tid) = 0u;
-    if (tid == 0) {
-      if (d.lse) d.lse[at] = -INFINITY;
-      if (a.lse2) a.lse2[at] = -INFINITY;
-    }
-    return;
-  }
-  const int64_t total = all * a.mult;
-  const int ctas = (int)min((int64_t)grid, total);
-  const int heads = 8 * a.octets;
-  const int prob = d.sel ? hh / heads : g * a.blocks + hh / heads;
-  // the numbers of its first and last tile, and the CTAs that have them
-  const int64_t s1 = start * a.mult + (prob + 1) * units - 1, s0 = s1 + 1 - units + kOverhead;
-  int c0 = (int)(s0 * ctas / total), c1 = (int)(s1 * ctas / total);
-  while (c0 + 1 < ctas && range_start(total, c0 + 1, ctas) <= s0) ++c0;
-  while (c1 + 1 < ctas && range_start(total, c1 + 1, ctas) <= s1) ++c1;
-  if (c0 == c1) return;  // written by its CTA
-  const int hrow = hh % heads, n = c1 - c0 + 1;
   const auto part = [&](int i) { return (2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0)) * 16 + hrow; };
   // the parts' weights exp2(m - M), their sum of sums
   float m = -INFINITY;
@@ -802,8 +831,8 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttnArgs a) {
   const PagedView& kv = d.kv;
   const int g = blockIdx.y, r = blockIdx.z;
   __shared__ float lse[64];
-  after_wait();
   const Entry n = entry_of(a, r);
+  after_wait();
   if (threadIdx.x < d.group) {
     const float y = a.lse2[(int64_t)r * d.Hq + g * d.group + threadIdx.x];
     lse[threadIdx.x] = y == -INFINITY ? INFINITY : y;
@@ -835,7 +864,7 @@ int device_sms() {
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Layout {
-  size_t prefix, lse2, ml, o, logits, total;
+  size_t prefix, split, lse2, ml, o, logits, total;
 };
 Layout layout_of(const rtp_paged_kv* kv, int n_rows, int n_q_heads, bool scores) {
   Layout l;
@@ -847,6 +876,7 @@ Layout layout_of(const rtp_paged_kv* kv, int n_rows, int n_q_heads, bool scores)
   };
   const size_t parts = (size_t)2 * kMaxPerSm * kMaxSms * 16;
   l.prefix = take(((size_t)n_rows * kv->n_kv_heads + 1) * sizeof(int64_t));
+  l.split = take((size_t)kMaxPerSm * kMaxSms * sizeof(int4));
   l.ml = take(parts * sizeof(float2));
   l.o = take(parts * kv->head_dim * sizeof(float));
   l.lse2 = take(scores ? (size_t)n_rows * n_q_heads * sizeof(float) : 0);
@@ -884,7 +914,7 @@ cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
   attn_kernel<QT, K, D, NB><<<(unsigned)grid, kThreads, smem, st>>>(a, km, vm);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const float bias = std::is_same_v<K, __nv_bfloat16> ? 0.f : 15.f;
-  e = launch_after(join_kernel<QT, D>, dim3(a.d.Hq, a.d.n_rows), kJoinWarps * 32, 0, st, a, (int)grid, bias);
+  e = launch_after(join_kernel<QT, D>, dim3((unsigned)grid, 8 * NB), kJoinWarps * 32, 0, st, a, bias);
   if (e != cudaSuccess || !a.logits) return e;
   const int64_t blocks = (a.cap + 1023) / 1024;
   return launch_after(weights_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024), a.d.kv.Hkv, a.d.n_rows), 256, 0,
@@ -916,6 +946,7 @@ cudaError_t launch_paged_decode(const DecodeArgs& d, const rtp_paged_kv* kv, int
   const Layout l = layout_of(kv, d.n_rows, d.Hq, d.scores != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(d.workspace);
   a.prefix = reinterpret_cast<int64_t*>(ws + l.prefix);
+  a.split = reinterpret_cast<int4*>(ws + l.split);
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   a.part_o = reinterpret_cast<float*>(ws + l.o);
   if (d.scores) {

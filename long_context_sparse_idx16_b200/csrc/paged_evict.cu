@@ -73,9 +73,14 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
 #pragma unroll 8
       for (int i = tid; i < n; i += kThreads) {
         const int p = pos[i];
-        keys[i] = __float_as_uint(sc[i]);
+        const float x = sc[i];
+        keys[i] = __float_as_uint(x);
         pos_s[i] = p;
         newest = max(newest, p);
+        if (apart && i < keep) {  // what stays; slots that are freed are written again below
+          a.out_scores[base + i] = x;
+          a.out_positions[base + i] = p;
+        }
       }
     } else {
 #pragma unroll 8
@@ -136,14 +141,18 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
       return ((unsigned long long)~((uint32_t)position(i) ^ 0x80000000u) << 32 | ~(uint32_t)i) >= tie_cut;
     };
 
-    // the lists: a warp takes a contiguous piece, counts, and writes behind the pieces before it
+    // the lists: a warp takes a contiguous piece, counts, and writes behind the pieces before it.  With
+    // the keys in shared memory a lane has at most 24 slots, whose verdicts it keeps as bits.
     int32_t* mover = a.moves + base;
     int32_t* hole = mover + (n - keep);
     const int per = (n + kThreads - 1) / kThreads * 32;
     const int i0 = warp * per, i1 = min(n, i0 + per);
+    const uint32_t below = (1u << lane) - 1u;
     int nm = 0, nh = 0;
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
+    uint32_t verdict = 0;
+    for (int i = i0 + lane, v = 0; i - lane < i1; i += 32, ++v) {
       const bool in = i < i1 && stays(i);
+      if (kSmem) verdict |= (uint32_t)in << v;
       nm += __popc(__ballot_sync(0xffffffffu, in && i >= keep));
       nh += __popc(__ballot_sync(0xffffffffu, i < i1 && !in && i < keep));
     }
@@ -153,16 +162,15 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
     int oh = block_exclusive(lane == 0 ? nh : 0, s.b, &holes);
     om = __shfl_sync(0xffffffffu, om, 0);
     oh = __shfl_sync(0xffffffffu, oh, 0);
-    const uint32_t below = (1u << lane) - 1u;
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
-      const bool in = i < i1 && stays(i);
+    for (int i = i0 + lane, v = 0; i - lane < i1; i += 32, ++v) {
+      const bool in = kSmem ? (verdict >> v) & 1u : i < i1 && stays(i);
       const bool mv = in && i >= keep, ho = i < i1 && !in && i < keep;
       const uint32_t bm = __ballot_sync(0xffffffffu, mv), bh = __ballot_sync(0xffffffffu, ho);
       if (mv) mover[om + __popc(bm & below)] = i;
       if (ho) hole[oh + __popc(bh & below)] = i;
       om += __popc(bm);
       oh += __popc(bh);
-      if (apart && in && i < keep) {
+      if (!kSmem && apart && in && i < keep) {
         a.out_scores[base + i] = sc[i];
         a.out_positions[base + i] = pos[i];
       }

@@ -98,6 +98,35 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
     for (int i = tid; i < u.count * kPageChunk; i += 32 * kScoreWarps) best[i] = 0u;
     if (tid == 0) s_max = 0u;
     uint32_t mag = 0u;
+    // the bounds of two tiles of 8 pages: B operands [tile][hi, lo][step][2]
+    uint32_t bb[2][2][KS][2];
+    const auto load_bounds = [&](int n0) {
+      const int pw = p0 + warp * kPagesPerWarp + n0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int p = pw + t * 8 + (lane >> 2);
+        const int64_t page = p < u.pages ? paged_page(kv, u.seq, p) : -1;
+        const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * D + (lane & 3) * E;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const uint4 v = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : ld_nc_u4(lim + (x ? 0 : D) + j * 4 * E);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (sizeof(K) == 1) {
+                bb[t][x][4 * j + e][0] = widen2<T>(w[e]);
+                bb[t][x][4 * j + e][1] = widen2<T>(w[e] >> 16);
+              } else {
+                bb[t][x][2 * j + (e >> 1)][e & 1] = w[e];
+              }
+            }
+          }
+      }
+    };
+    const int n_mine = min(kPagesPerWarp, u.pages - (p0 + warp * kPagesPerWarp));  // pages of this warp
+    if (n_mine > 0) load_bounds(0);  // in flight while the queries are laid out
     // the run's heads, m_pad at a time (all of them, unless groups are large)
     for (int m0 = 0; m0 < m_rows; m0 += m_pad) {
       const int m_n = min(m_rows - m0, m_pad), m_tiles = (m_n + 15) / 16;
@@ -116,34 +145,13 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
         *(uint32_t*)(at + m_pad * QS + 16) = neg_part<T>(v.y);
       }
       __syncthreads();
-      for (int n0 = 0; n0 < kPagesPerWarp; n0 += 16) {
-        const int pw = p0 + warp * kPagesPerWarp + n0;
-        if (pw >= u.pages) break;
-        // the bounds of two tiles of 8 pages: B operands [tile][hi, lo][step][2]
-        uint32_t bb[2][2][KS][2];
+      for (int n0 = 0; n0 < n_mine; n0 += 16) {
+        if (n0 > 0 || m0 > 0) load_bounds(n0);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int p = pw + t * 8 + (lane >> 2);
-          const int64_t page = p < u.pages ? paged_page(kv, u.seq, p) : -1;
-          const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * D + (lane & 3) * E;
-          if (p < u.pages && page < 0 && (lane & 3) == 0)  // no number: the exact path ranks it last
-            for (int i = 0; i < u.count; ++i) atomicMax(&best[i * kPageChunk + p - p0], 0xffffffffu);
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-              const uint4 v = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : ld_nc_u4(lim + (x ? 0 : D) + j * 4 * E);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if constexpr (sizeof(K) == 1) {
-                  bb[t][x][4 * j + e][0] = widen2<T>(w[e]);
-                  bb[t][x][4 * j + e][1] = widen2<T>(w[e] >> 16);
-                } else {
-                  bb[t][x][2 * j + (e >> 1)][e & 1] = w[e];
-                }
-              }
-            }
+        for (int t = 0; t < 2; ++t) {  // pages outside the pool: no number, which the exact path ranks last
+          const int p = n0 + t * 8 + (lane >> 2);
+          if (p < n_mine && (lane & 3) == 0 && paged_page(kv, u.seq, p0 + warp * kPagesPerWarp + p) < 0)
+            for (int i = 0; i < u.count; ++i) atomicMax(&best[i * kPageChunk + warp * kPagesPerWarp + p], 0xffffffffu);
         }
         if (m0 == 0) {
 #pragma unroll
@@ -247,9 +255,10 @@ struct PickShared {
   unsigned long long key[kMaxBetween];
 };
 
-// Exact key of a page, by one warp; 0 (last) for a page outside the pool or a score that is no number.
+// Exact order key of one head's score in a page, by one warp; 0 (last) for a page outside the pool,
+// ~0 for a score that is no number (one such head makes the page rank last).
 template <typename T, typename K>
-__device__ unsigned long long exact_key(const SelectPagesArgs& a, const T* q, int seq, int g, int p) {
+__device__ __forceinline__ unsigned long long exact_key(const SelectPagesArgs& a, const T* q, int seq, int g, int p) {
   const PagedView& kv = a.kv;
   const int lane = threadIdx.x & 31;
   const int64_t page = paged_page(kv, seq, p);
@@ -258,28 +267,16 @@ __device__ unsigned long long exact_key(const SelectPagesArgs& a, const T* q, in
     return 0ull;
   }
   const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * kv.D;
-  double lo[4], hi[4];
+  double s = 0.0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int d = e * 32 + lane;
-    lo[e] = d < kv.D ? to_f32(lim[d]) : 0.f;
-    hi[e] = d < kv.D ? to_f32(lim[kv.D + d]) : 0.f;
+    const double x = d < kv.D ? to_f32(q[d]) : 0.f;
+    const double lo = d < kv.D ? to_f32(lim[d]) : 0.f, hi = d < kv.D ? to_f32(lim[kv.D + d]) : 0.f;
+    s += x * (x < 0.0 ? lo : hi);
   }
-  double best = -INFINITY;
-  bool nan = false;
-  for (int u = 0; u < a.group; ++u) {
-    double s = 0.0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int d = e * 32 + lane;
-      const double x = d < kv.D ? to_f32(q[u * kv.D + d]) : 0.f;
-      s += x * (x < 0.0 ? lo[e] : hi[e]);
-    }
-    s = warp_sum(s);
-    nan |= s != s;
-    best = fmax(best, s);
-  }
-  return nan ? 0ull : order_key64(best);
+  s = warp_sum(s);
+  return s != s ? ~0ull : order_key64(s);
 }
 
 // One CTA of kT threads per (KV head, row); the scores in shared memory, or in the workspace itself.
@@ -290,8 +287,9 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
   const PagedView& kv = a.kv;
   const int g = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < kBins; i += kT) s.hist[i] = 0;
+  for (int i = tid; i < kMaxBetween; i += kT) s.key[i] = 0ull;
   if (tid == 0) s.got = 0;
-  after_wait();
+  // the operator's inputs may be read ahead of the scores, its outputs be written
   int seq;
   const int len = paged_row(kv, a.row_seq, a.row_len, r, &seq);
   if (g == 0 && tid == 0 && paged_row_bad(kv, a.row_seq, a.row_len, r)) paged_err(kv, RTP_PAGED_ERANGE);
@@ -310,9 +308,18 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
   float lo = 0.f, scale = 0.f;
   int cut = kBins;
   const auto bin_of = [&](float y) { return min(kBins - 1, (int)((y - lo) * scale)); };
-  if (want > 0 && want < c1 - c0) {
+  const bool choose = want > 0 && want < c1 - c0;
+  float q1 = 0.f;  // the greatest |q|_1 of the heads
+  if (choose)
+    for (int u = warp; u < a.group; u += kT / 32) {
+      float y = 0.f;
+      for (int d = lane; d < kv.D; d += 32) y += fabsf(to_f32(q[u * kv.D + d]));
+      q1 = fmaxf(q1, warp_sum(y));
+    }
+  after_wait();
+  if (choose) {
     // the scores' range; eps
-    float low = INFINITY, high = -INFINITY, mag = 0.f, q1 = 0.f;
+    float low = INFINITY, high = -INFINITY, mag = 0.f;
     bool odd = false;
 #pragma unroll 4
     for (int i = c0 + tid; i < c1; i += kT) {
@@ -323,11 +330,6 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
       odd |= !isfinite(y);
     }
     for (int i = tid; i < chunks && i * kPageChunk < pages; i += kT) mag = fmaxf(mag, a.chunk_max[prob * chunks + i]);
-    for (int u = warp; u < a.group; u += kT / 32) {
-      float y = 0.f;
-      for (int d = lane; d < kv.D; d += 32) y += fabsf(to_f32(q[u * kv.D + d]));
-      q1 = fmaxf(q1, warp_sum(y));
-    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
@@ -386,10 +388,14 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
         if (b >= bin - 1 && b <= bin + 1) s.idx[atomicAdd(&s.got, 1)] = i;
       }
       __syncthreads();
-      for (int j = warp; j < m; j += kT / 32) {
-        const unsigned long long k = exact_key<T, K>(a, q, seq, g, s.idx[j]);
-        if (lane == 0) s.key[j] = k;
+      // a warp per page and head; the greatest head's key
+      for (int j = warp; j < m * a.group; j += kT / 32) {
+        const unsigned long long k = exact_key<T, K>(a, q + j % a.group * kv.D, seq, g, s.idx[j / a.group]);
+        if (lane == 0) atomicMax(&s.key[j / a.group], k);
       }
+      __syncthreads();
+      for (int j = tid; j < m; j += kT)
+        if (s.key[j] == ~0ull) s.key[j] = 0ull;
       __syncthreads();
       for (int j = tid; j < m; j += kT) {
         const unsigned long long k = s.key[j];
@@ -403,8 +409,9 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
       // every page by its exact score
       unsigned long long* keys = a.keys + prob * kv.max_pages;
       for (int i = c0 + warp; i < c1; i += kT / 32) {
-        const unsigned long long k = exact_key<T, K>(a, q, seq, g, i);
-        if (lane == 0) keys[i] = k;
+        unsigned long long k = 0ull;
+        for (int u = 0; u < a.group; ++u) k = max(k, exact_key<T, K>(a, q + u * kv.D, seq, g, i));
+        if (lane == 0) keys[i] = k == ~0ull ? 0ull : k;
       }
       __syncthreads();
       int ties;
