@@ -269,8 +269,8 @@ struct SelectPagesArgs {
   float* approx;             // workspace [n_rows][Hkv][max_pages]
   float* chunk_max;          // workspace [n_rows][Hkv][page_chunks(max_pages)]
 };
-// pages that one CTA of the page scoring takes
-constexpr int kPageChunk = 256;
+// pages that a warp of the page scoring takes at a time
+constexpr int kPageChunk = 16;
 inline int page_chunks(int max_pages) { return (max_pages + kPageChunk - 1) / kPageChunk; }
 
 struct EvictArgs {

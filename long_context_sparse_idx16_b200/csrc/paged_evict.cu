@@ -43,7 +43,7 @@ __device__ void find_bin(PickShared& s, int want) {
     s.above = before + c0;
     s.exact = before + c0 + c1 == want;
   }
-  __syncthreads();
+  __syncthreads();  // (the caller's next write of hist lies behind another one)
 }
 
 template <bool kSmem>
@@ -51,7 +51,10 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
   extern __shared__ uint32_t keys[];  // [n] keys, then [n] positions
   __shared__ PickShared s;
   const PagedView& kv = a.kv;
-  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) s.newest = INT32_MIN;
+  for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+  __syncthreads();
   after_wait();
   const int64_t prob = (int64_t)b * kv.Hkv + g, base = prob * a.stride;
   const float* sc = a.scores + base;
@@ -63,32 +66,40 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
   if (g == 0 && tid == 0) a.out_len[b] = keep;
   const bool apart = a.out_scores != a.scores || a.out_positions != a.positions;
   int moved = 0;
-  if (keep < n) {
-    if (tid == 0) s.newest = INT32_MIN;
-    __syncthreads();
+  int32_t* pos_s = reinterpret_cast<int32_t*>(keys + n);
+  // One pass over the arrays, in batches that are in flight together: the newest position; what stays
+  // is copied (slots that are freed are written again below); scores and positions are kept.
+  {
+    constexpr int kBatch = 8;
     int newest = INT32_MIN;
-    int32_t* pos_s = reinterpret_cast<int32_t*>(keys + n);
-    if (kSmem) {
-      // both arrays in one go, scores as they are; then newest is known and the keys are formed
-#pragma unroll 8
-      for (int i = tid; i < n; i += kThreads) {
-        const int p = pos[i];
-        const float x = sc[i];
-        keys[i] = __float_as_uint(x);
-        pos_s[i] = p;
-        newest = max(newest, p);
-        if (apart && i < keep) {  // what stays; slots that are freed are written again below
-          a.out_scores[base + i] = x;
-          a.out_positions[base + i] = p;
+    const int end = keep < n ? n : apart ? keep : 0;
+    for (int i0 = tid; i0 < end; i0 += kThreads * kBatch) {
+      float x[kBatch];
+      int p[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * kThreads;
+        x[u] = i < end ? sc[i] : 0.f;
+        p[u] = i < end ? pos[i] : INT32_MIN;
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * kThreads;
+        newest = max(newest, p[u]);
+        if (i < end && kSmem && keep < n) {
+          keys[i] = __float_as_uint(x[u]);
+          pos_s[i] = p[u];
+        }
+        if (apart && i < keep) {
+          a.out_scores[base + i] = x[u];
+          a.out_positions[base + i] = p[u];
         }
       }
-    } else {
-#pragma unroll 8
-      for (int i = tid; i < n; i += kThreads) newest = max(newest, pos[i]);
     }
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) atomicMax(&s.newest, newest);
-    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+  }
+  if (keep < n) {
     __syncthreads();
     const int64_t recent = (int64_t)s.newest - a.n_recent;
     const auto position = [&](int i) -> int { return kSmem ? pos_s[i] : pos[i]; };
@@ -124,7 +135,6 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
       cut |= (uint32_t)s.bin << shift;
       want -= s.above;
       whole = s.exact != 0;
-      __syncthreads();
     }
     // ties: of the slots whose key is the cut, the `want` of lowest (position, slot)
     unsigned long long tie_cut = 0;
@@ -141,53 +151,50 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
       return ((unsigned long long)~((uint32_t)position(i) ^ 0x80000000u) << 32 | ~(uint32_t)i) >= tie_cut;
     };
 
-    // the lists: a warp takes a contiguous piece, counts, and writes behind the pieces before it.  With
-    // the keys in shared memory a lane has at most 24 slots, whose verdicts it keeps as bits.
+    // The lists, in slot order: a thread takes an odd number of successive slots (no bank conflicts),
+    // counts its movers and holes, and writes them behind those of the threads before it.
     int32_t* mover = a.moves + base;
     int32_t* hole = mover + (n - keep);
-    const int per = (n + kThreads - 1) / kThreads * 32;
-    const int i0 = warp * per, i1 = min(n, i0 + per);
-    const uint32_t below = (1u << lane) - 1u;
+    const int per = (n + kThreads - 1) / kThreads | 1;
+    const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
     int nm = 0, nh = 0;
-    uint32_t verdict = 0;
-    for (int i = i0 + lane, v = 0; i - lane < i1; i += 32, ++v) {
-      const bool in = i < i1 && stays(i);
-      if (kSmem) verdict |= (uint32_t)in << v;
-      nm += __popc(__ballot_sync(0xffffffffu, in && i >= keep));
-      nh += __popc(__ballot_sync(0xffffffffu, i < i1 && !in && i < keep));
+    uint32_t verdict = 0;  // with the keys in shared memory a thread has at most 25 slots
+    for (int i = i0; i < i1; ++i) {
+      const bool in = stays(i);
+      if (kSmem) verdict |= (uint32_t)in << (i - i0);
+      nm += in && i >= keep;
+      nh += !in && i < keep;
     }
     int holes;
-    // the sums over warps: each warp's lane 0 carries its count
-    int om = block_exclusive(lane == 0 ? nm : 0, s.a, &moved);
-    int oh = block_exclusive(lane == 0 ? nh : 0, s.b, &holes);
-    om = __shfl_sync(0xffffffffu, om, 0);
-    oh = __shfl_sync(0xffffffffu, oh, 0);
-    for (int i = i0 + lane, v = 0; i - lane < i1; i += 32, ++v) {
-      const bool in = kSmem ? (verdict >> v) & 1u : i < i1 && stays(i);
-      const bool mv = in && i >= keep, ho = i < i1 && !in && i < keep;
-      const uint32_t bm = __ballot_sync(0xffffffffu, mv), bh = __ballot_sync(0xffffffffu, ho);
-      if (mv) mover[om + __popc(bm & below)] = i;
-      if (ho) hole[oh + __popc(bh & below)] = i;
-      om += __popc(bm);
-      oh += __popc(bh);
-      if (!kSmem && apart && in && i < keep) {
-        a.out_scores[base + i] = sc[i];
-        a.out_positions[base + i] = pos[i];
-      }
+    int om = block_exclusive(nm, s.a, &moved);
+    int oh = block_exclusive(nh, s.b, &holes);
+    for (int i = i0; i < i1; ++i) {
+      const bool in = kSmem ? (verdict >> (i - i0)) & 1u : stays(i);
+      if (in && i >= keep) mover[om++] = i;
+      if (!in && i < keep) hole[oh++] = i;
     }
     __syncthreads();
     // what moves in: the sources lie at or behind the budget, where nothing has been written yet
-    for (int m = tid; m < moved; m += kThreads) {
-      const int to = hole[m], from = mover[m];
-      a.out_scores[base + to] = sc[from];
-      a.out_positions[base + to] = pos[from];
+    constexpr int kBatch = 4;
+    for (int m0 = tid; m0 < moved; m0 += kThreads * kBatch) {
+      int to[kBatch], from[kBatch];
+      float x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int m = m0 + u * kThreads;
+        to[u] = m < moved ? hole[m] : 0;
+        from[u] = m < moved ? mover[m] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) x[u] = sc[from[u]];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (m0 + u * kThreads < moved) {
+          a.out_scores[base + to[u]] = x[u];
+          a.out_positions[base + to[u]] = position(from[u]);
+        }
     }
     __syncthreads();
-  } else if (apart) {
-    for (int i = tid; i < keep; i += kThreads) {
-      a.out_scores[base + i] = sc[i];
-      a.out_positions[base + i] = pos[i];
-    }
   }
   if (tid == 0) a.n_moves[prob] = moved;
   for (int64_t i = keep + tid; i < a.stride; i += kThreads) {

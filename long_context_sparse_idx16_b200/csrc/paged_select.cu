@@ -15,6 +15,7 @@
 // The bounds are read once per row (once per eight rows of a sequence that follow one another),
 // 4 D bytes a page in 16 bits: HBM bounds the scoring of decode rows, the tensor cores that of chunks.
 #include "paged.cuh"
+#include "tc_umma.cuh"
 
 namespace rtp {
 
@@ -23,9 +24,9 @@ namespace {
 // ---- scores
 
 constexpr int kScoreWarps = 8;
-constexpr int kPagesPerWarp = kPageChunk / kScoreWarps;  // 32
-constexpr int kRowBlock = 8;  // rows of a chunk that share one read of the bounds
-constexpr int kMaxM = 64 + 16 * kRowBlock;  // heads of a run of rows that are kept at once
+constexpr int kRowBlock = 8;  // rows of a chunk that share one read of the bounds, at most
+constexpr int kMaxM = 192;    // heads of these rows, at most
+constexpr int kCtaPages = kScoreWarps * kPageChunk;
 
 template <typename T>
 using pair_t = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
@@ -70,172 +71,200 @@ __device__ __forceinline__ Run run_at(const SelectPagesArgs& a, int r, int end) 
   return u;
 }
 
-// One CTA: a chunk of pages, a KV head, a block of rows.  A warp takes 32 pages, 16 at a time: a lane
-// holds E = 16 bytes' worth of successive dims of page (lane / 4) of an 8-page tile, dims
-// (4 j + lane % 4) E ... of load j.  The queries lie in shared memory in the order of the
-// contraction that this gives, max(q, 0) and min(q, 0) apart, rows 16 bytes off a multiple of 128.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(mbar)
+               : "memory");
+}
+
+// One CTA: a KV head, a block of rows, `rounds` times 128 pages.  The rows' queries are laid out in
+// shared memory in the order of the contraction, max(q, 0) and min(q, 0) apart; from there on the warps
+// work by themselves, 16 pages at a time.  A lane copies half of one page's bounds (its lo or its hi
+// row) to the warp's piece of shared memory, so that 16 pages are in flight at once; rows there are 16
+// bytes off a multiple of 128, which ldmatrix reads without conflicts.  The bounds go to registers for
+// all of the heads, and the next 16 pages are on their way meanwhile.
 template <typename T, typename K, int D>
-__global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const SelectPagesArgs a, int row_block, int m_pad) {
-  constexpr int E = 16 / (int)sizeof(K);
-  constexpr int J = D / (4 * E);  // loads per bound
-  constexpr int KS = D / 16;      // steps of 16 terms per bound
-  constexpr int QS = 2 * D + 16;  // bytes between query rows
+struct Score {
+  static constexpr int kB = 2 * D * (int)sizeof(K);  // bytes of a page's bounds
+  static constexpr int kBS = kB + 16;
+  static constexpr int kQS = 2 * D + 16;             // bytes between query rows
+  static size_t smem(int m_pad, int row_block) {
+    return (size_t)kCtaPages * kBS + (size_t)2 * m_pad * kQS + (size_t)row_block * kCtaPages * sizeof(uint32_t);
+  }
+};
+
+template <typename T, typename K, int D>
+__global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const SelectPagesArgs a, int row_block, int m_pad,
+                                                                      int rounds, int chunks) {
+  using S = Score<T, K, D>;
+  constexpr bool k8 = sizeof(K) == 1;
+  constexpr int KS = D / 16;  // steps of 16 terms per bound
   extern __shared__ __align__(16) uint8_t smem_[];
-  uint8_t* sq = smem_;                                                            // [2][m_pad][QS]
-  uint32_t* best = reinterpret_cast<uint32_t*>(smem_ + (size_t)2 * m_pad * QS);   // [row_block][kPageChunk]
-  __shared__ uint32_t s_max;
+  uint8_t* sq = smem_ + kCtaPages * S::kBS;                                           // [2][m_pad][kQS]
+  __shared__ unsigned long long bar[kScoreWarps];
   const PagedView& kv = a.kv;
   const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* sb = smem_ + warp * kPageChunk * S::kBS;                                   // [kPageChunk][kBS], this warp's
+  uint32_t* best = reinterpret_cast<uint32_t*>(sq + (size_t)2 * m_pad * S::kQS) + warp * kPageChunk;  // [row_block][kCtaPages]
   const int r_end = min(a.n_rows, ((int)blockIdx.z + 1) * row_block);
+  const uint32_t landed = smem_u32(&bar[warp]);
+  if (lane == 0) {
+    mbar_init(landed, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  uint32_t phase = 0;
   after_wait();
   for (int r = blockIdx.z * row_block; r < r_end;) {
     const Run u = run_at(a, r, r_end);
     r += u.count;
-    const int p0 = blockIdx.x * kPageChunk;
-    if (p0 >= u.pages) continue;  // the whole CTA alike
-    const int m_rows = u.count * a.group;
+    const int first = blockIdx.x * rounds * kCtaPages;
+    if (first >= u.pages) continue;  // the whole CTA alike
+    // copies of 16 pages from p on; whether this lane's page (lane % 16) lies outside the pool
+    const auto start = [&](int p) -> bool {
+      const bool live = p + (lane & 15) < u.pages;
+      const int64_t page = live ? paged_page(kv, u.seq, p + (lane & 15)) : -1;
+      const int n_load = __popc(__ballot_sync(0xffffffffu, page >= 0));
+      uint8_t* to = sb + (lane & 15) * S::kBS + (lane >> 4) * (S::kB / 2);
+      if (page < 0)  // pages left out: zeros
+        for (int x = 0; x < S::kB / 32; ++x) ((uint4*)to)[x] = make_uint4(0u, 0u, 0u, 0u);
+      if (lane == 0) mbar_expect_tx(landed, n_load * (S::kB / 2));
+      __syncwarp();
+      fence_async_smem();  // zeros of an earlier round lie behind this copy
+      if (page >= 0)
+        bulk_load(smem_u32(to), (const K*)kv.bounds + ((page * kv.Hkv + g) * 2 + (lane >> 4)) * D, S::kB / 2, landed);
+      return live && page < 0;
+    };
+    int p = first + warp * kPageChunk;
+    bool bad = false;
+    if (p < u.pages) bad = start(p);
+    const int m_rows = u.count * a.group, m_tiles = (m_rows + 15) / 16;
+    __syncthreads();  // the last run's queries have been read
+    for (int i = tid; i < m_tiles * 16 * (D / 4); i += 32 * kScoreWarps) {
+      // four dims: 16-bit bounds in order; for e4m3, lane c's pair of pairs of step k, two slots at
+      // 2 c and two at 8 + 2 c, as ldmatrix delivers the bounds' bytes
+      const int m = i / (D / 4), d = i % (D / 4) * 4;
+      uint2 v = make_uint2(0u, 0u);
+      if (m < m_rows)
+        v = *(const uint2*)((const T*)a.q + (u.first + m / a.group) * a.q_stride +
+                            (int64_t)(g * a.group + m % a.group) * D + d);
+      uint8_t* at = sq + m * S::kQS + (k8 ? d / 16 * 32 + d % 16 : d * 2);
+      const int second = k8 ? 16 : 4;
+      *(uint32_t*)at = pos_part<T>(v.x);
+      *(uint32_t*)(at + second) = pos_part<T>(v.y);
+      *(uint32_t*)(at + m_pad * S::kQS) = neg_part<T>(v.x);
+      *(uint32_t*)(at + m_pad * S::kQS + second) = neg_part<T>(v.y);
+    }
     __syncthreads();
-    for (int i = tid; i < u.count * kPageChunk; i += 32 * kScoreWarps) best[i] = 0u;
-    if (tid == 0) s_max = 0u;
-    uint32_t mag = 0u;
-    // the bounds of two tiles of 8 pages: B operands [tile][hi, lo][step][2]
-    uint32_t bb[2][2][KS][2];
-    const auto load_bounds = [&](int n0) {
-      const int pw = p0 + warp * kPagesPerWarp + n0;
+    for (int round = 0; round < rounds && p < u.pages; ++round, p += kCtaPages) {
+      if (!mbar_wait(landed, phase) && lane == 0) paged_err(kv, RTP_PAGED_ETIMEOUT);
+      phase ^= 1u;
+      __syncwarp();  // the other lanes' zeros
+      uint32_t bb[2][2][KS][2];  // B operands [tile of 8 pages][hi, lo][step][2]
+      uint32_t mag = 0u;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int p = pw + t * 8 + (lane >> 2);
-        const int64_t page = p < u.pages ? paged_page(kv, u.seq, p) : -1;
-        const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * D + (lane & 3) * E;
+        // matrices of 8 pages by 16 bytes, four along the bounds: lo, then hi
+        const uint32_t bt = smem_u32(sb + (t * 8 + (lane & 7)) * S::kBS + (lane >> 3) * 16);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int j = 0; j < J; ++j) {
-            const uint4 v = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : ld_nc_u4(lim + (x ? 0 : D) + j * 4 * E);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int k = 0; k < KS; k += k8 ? 4 : 2) {
+            uint32_t w[4];
+            ldsm_x4(bt + (1 - x) * D * (int)sizeof(K) + k * 16 * (int)sizeof(K), w[0], w[1], w[2], w[3]);
+            if constexpr (k8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (sizeof(K) == 1) {
-                bb[t][x][4 * j + e][0] = widen2<T>(w[e]);
-                bb[t][x][4 * j + e][1] = widen2<T>(w[e] >> 16);
-              } else {
-                bb[t][x][2 * j + (e >> 1)][e & 1] = w[e];
+              for (int e = 0; e < 4; ++e) {
+                bb[t][x][k + e][0] = widen2<T>(w[e]);
+                bb[t][x][k + e][1] = widen2<T>(w[e] >> 16);
               }
+            } else {
+              bb[t][x][k][0] = w[0];
+              bb[t][x][k][1] = w[1];
+              bb[t][x][k + 1][0] = w[2];
+              bb[t][x][k + 1][1] = w[3];
             }
           }
-      }
-    };
-    const int n_mine = min(kPagesPerWarp, u.pages - (p0 + warp * kPagesPerWarp));  // pages of this warp
-    if (n_mine > 0) load_bounds(0);  // in flight while the queries are laid out
-    // the run's heads, m_pad at a time (all of them, unless groups are large)
-    for (int m0 = 0; m0 < m_rows; m0 += m_pad) {
-      const int m_n = min(m_rows - m0, m_pad), m_tiles = (m_n + 15) / 16;
-      __syncthreads();
-      for (int i = tid; i < m_tiles * 16 * (D / 4); i += 32 * kScoreWarps) {
-        // four dims: lane c's share of step k, two slots at 2 c and two at 8 + 2 c
-        const int m = i / (D / 4), d = i % (D / 4) * 4, c = d / E % 4, k = d / (4 * E) * (E / 4) + d % E / 4;
-        uint2 v = make_uint2(0u, 0u);
-        if (m < m_n)
-          v = *(const uint2*)((const T*)a.q + (u.first + (m0 + m) / a.group) * a.q_stride +
-                              (int64_t)(g * a.group + (m0 + m) % a.group) * D + d);
-        uint8_t* at = sq + m * QS + k * 32 + c * 4;
-        *(uint32_t*)at = pos_part<T>(v.x);
-        *(uint32_t*)(at + 16) = pos_part<T>(v.y);
-        *(uint32_t*)(at + m_pad * QS) = neg_part<T>(v.x);
-        *(uint32_t*)(at + m_pad * QS + 16) = neg_part<T>(v.y);
-      }
-      __syncthreads();
-      for (int n0 = 0; n0 < n_mine; n0 += 16) {
-        if (n0 > 0 || m0 > 0) load_bounds(n0);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {  // pages outside the pool: no number, which the exact path ranks last
-          const int p = n0 + t * 8 + (lane >> 2);
-          if (p < n_mine && (lane & 3) == 0 && paged_page(kv, u.seq, p0 + warp * kPagesPerWarp + p) < 0)
-            for (int i = 0; i < u.count; ++i) atomicMax(&best[i * kPageChunk + warp * kPagesPerWarp + p], 0xffffffffu);
-        }
-        if (m0 == 0) {
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int k = 0; k < KS; ++k) mag = abs_max<T>(abs_max<T>(mag, bb[t][x][k][0]), bb[t][x][k][1]);
+      }
+      // The greatest magnitude of the 16 pages' bounds.  It depends on every value read, so the copy of
+      // the next 16 pages behind it cannot overtake the reads.
+      {
+        const T* h = reinterpret_cast<const T*>(&mag);
+        const float x = fmaxf(to_f32(h[0]), to_f32(h[1]));
+        const uint32_t y = __reduce_max_sync(0xffffffffu, __float_as_uint(x));  // not negative: bits order alike
+        if (lane < u.count)
+          a.chunk_max[((int64_t)(u.first + lane) * kv.Hkv + g) * chunks + p / kPageChunk] = __uint_as_float(y);
+      }
+      const bool bad_now = bad;
+      if (round + 1 < rounds && p + kCtaPages < u.pages) bad = start(p + kCtaPages);
+      for (int i = lane; i < u.count * kPageChunk; i += 32) best[i / kPageChunk * kCtaPages + i % kPageChunk] = 0u;
+      __syncwarp();
+#pragma unroll 1
+      for (int mt = 0; mt < m_tiles; ++mt) {
+        // c[t][e]: head lane / 4 + 8 (e / 2), page 8 t + 2 (lane % 4) + e % 2
+        float c[2][4] = {};
+        const uint32_t at = smem_u32(sq + (mt * 16 + (lane & 15)) * S::kQS + (lane >> 4) * 16);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t f[4];
+            ldsm_x4(at + x * m_pad * S::kQS + k * 32, f[0], f[1], f[2], f[3]);
+            mma<T>(c[0], f, bb[0][x][k][0], bb[0][x][k][1]);
+            mma<T>(c[1], f, bb[1][x][k][0], bb[1][x][k][1]);
+          }
+        // the greatest head of each row, as order keys (a NaN of the products is the greatest key)
+        if ((a.group & 7) == 0) {
+          // eight heads of a row in the eight lanes of a page: halved three times, each lane ends with
+          // one of the eight (row half, tile, page parity) combinations
+          uint32_t key[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) key[x] = order_key(c[(x >> 1) & 1][(x & 1) + (x >> 2) * 2]);
+          const int hi2 = (lane >> 4) & 1, hi1 = (lane >> 3) & 1, hi0 = (lane >> 2) & 1;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t own = hi2 ? key[x + 4] : key[x], other = hi2 ? key[x] : key[x + 4];
+            key[x] = max(own, __shfl_xor_sync(0xffffffffu, other, 16));
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t own = hi1 ? key[x + 2] : key[x], other = hi1 ? key[x] : key[x + 2];
+            key[x] = max(own, __shfl_xor_sync(0xffffffffu, other, 8));
+          }
+          const uint32_t own = hi0 ? key[1] : key[0], other = hi0 ? key[0] : key[1];
+          const uint32_t top = max(own, __shfl_xor_sync(0xffffffffu, other, 4));
+          const int m = mt * 16 + hi2 * 8;
+          uint32_t* to = best + hi1 * 8 + (lane & 3) * 2 + hi0;
+          if (a.group == 8) {
+            if (m < m_rows) to[(m >> 3) * kCtaPages] = top;  // all of the row's heads
+          } else if (m < m_rows) {
+            atomicMax(to + m / a.group * kCtaPages, top);
+          }
+        } else {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int k = 0; k < KS; ++k) mag = abs_max<T>(abs_max<T>(mag, bb[t][x][k][0]), bb[t][x][k][1]);
-        }
-        __syncwarp();
-        uint32_t* out = best + warp * kPagesPerWarp + n0;  // [row][page of this warp's 16]
-#pragma unroll 1
-        for (int mt = 0; mt < m_tiles; ++mt) {
-          float c[2][4] = {};
-          const uint32_t at = smem_u32(sq + (mt * 16 + (lane & 15)) * QS + (lane >> 4) * 16);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            uint32_t f[4];
-            ldsm_x4(at + k * 32, f[0], f[1], f[2], f[3]);
-            mma<T>(c[0], f, bb[0][0][k][0], bb[0][0][k][1]);
-            mma<T>(c[1], f, bb[1][0][k][0], bb[1][0][k][1]);
-            ldsm_x4(at + m_pad * QS + k * 32, f[0], f[1], f[2], f[3]);
-            mma<T>(c[0], f, bb[0][1][k][0], bb[0][1][k][1]);
-            mma<T>(c[1], f, bb[1][1][k][0], bb[1][1][k][1]);
-          }
-          // the greatest head of each row, as order keys (a NaN of the products is the greatest key).
-          // c[t][e]: head lane / 4 + 8 (e / 2), page 8 t + 2 (lane % 4) + e % 2
-          const int m = m0 + mt * 16 + (lane >> 2);
-          if ((a.group & 7) == 0) {
-            // eight heads of a row in the eight lanes of a page: halved three times, each lane ends
-            // with one of the eight (row half, tile, page parity) combinations
-            uint32_t key[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) key[x] = order_key(c[(x >> 1) & 1][(x & 1) + (x >> 2) * 2]);
-            const int hi2 = (lane >> 4) & 1, hi1 = (lane >> 3) & 1, hi0 = (lane >> 2) & 1;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t mine = hi2 ? key[x + 4] : key[x], other = hi2 ? key[x] : key[x + 4];
-              key[x] = max(mine, __shfl_xor_sync(0xffffffffu, other, 16));
+            for (int e = 0; e < 4; ++e) {
+              const int m = mt * 16 + (lane >> 2) + (e >> 1) * 8;
+              if (m < m_rows)
+                atomicMax(best + m / a.group * kCtaPages + t * 8 + (lane & 3) * 2 + (e & 1), order_key(c[t][e]));
             }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t mine = hi1 ? key[x + 2] : key[x], other = hi1 ? key[x] : key[x + 2];
-              key[x] = max(mine, __shfl_xor_sync(0xffffffffu, other, 8));
-            }
-            const uint32_t mine = hi0 ? key[1] : key[0], other = hi0 ? key[0] : key[1];
-            const uint32_t top = max(mine, __shfl_xor_sync(0xffffffffu, other, 4));
-            const int row = m0 + mt * 16 + hi2 * 8;
-            if (row < m_rows) {
-              uint32_t* to = out + row / a.group * kPageChunk + hi1 * 8 + (lane & 3) * 2 + hi0;
-              if (a.group == 8) *to = max(*to, top);  // nobody else writes it now
-              else atomicMax(to, top);
-            }
-          } else {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int x = m + (e >> 1) * 8;
-                if (x < m_rows)
-                  atomicMax(out + x / a.group * kPageChunk + t * 8 + (lane & 3) * 2 + (e & 1), order_key(c[t][e]));
-              }
-          }
         }
       }
-    }
-    // magnitude of the bounds seen
-    {
-      const T* h = reinterpret_cast<const T*>(&mag);
-      const float x = fmaxf(to_f32(h[0]), to_f32(h[1]));
-      const uint32_t y = __reduce_max_sync(0xffffffffu, __float_as_uint(x));  // not negative: bits order alike
-      if (lane == 0) atomicMax(&s_max, y);
-    }
-    __syncthreads();
-    for (int i = tid; i < u.count * kPageChunk; i += 32 * kScoreWarps) {
-      const int row = u.first + i / kPageChunk, p = p0 + i % kPageChunk;
-      if (p < u.pages) {
-        const uint32_t key = best[i];
-        a.approx[((int64_t)row * kv.Hkv + g) * kv.max_pages + p] =
-            key == 0xffffffffu ? __uint_as_float(0x7fc00000u) : key_to_float(key);
+      __syncwarp();
+      // two rows of 16 pages at a time; no number for a page outside the pool: the exact path ranks it last
+      for (int i = lane >> 4; i < u.count; i += 2) {
+        const uint32_t key = best[i * kCtaPages + (lane & 15)];
+        if (p + (lane & 15) < u.pages)
+          a.approx[((int64_t)(u.first + i) * kv.Hkv + g) * kv.max_pages + p + (lane & 15)] =
+              bad_now || key == 0xffffffffu ? __uint_as_float(0x7fc00000u) : key_to_float(key);
       }
+      __syncwarp();
     }
-    for (int i = tid; i < u.count; i += 32 * kScoreWarps)
-      a.chunk_max[((int64_t)(u.first + i) * kv.Hkv + g) * gridDim.x + blockIdx.x] = __uint_as_float(s_max);
   }
 }
 
@@ -243,52 +272,78 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
 
 constexpr int kBins = 1024;
 constexpr int kMaxBetween = 256;  // pages ranked by their exact scores in shared memory
-constexpr int kPagesInSmem = 48 * 1024;
+constexpr int kPagesInSmem = 40 * 1024;
+
+constexpr int kExactPages = 16;   // pages whose bounds are staged at a time for their exact scores
+constexpr int kMaxPer = 25;       // pages a thread keeps its verdicts of
 
 struct PickShared {
   uint32_t hist[kBins];
   uint32_t small[257];
-  float f[4][32];
+  uint32_t low, high, mag, q1;      // order keys of the scores' range; bits of the magnitudes
   int sums[33];
   int bin, n_in, n_between, got;
-  int idx[kMaxBetween];
+  int idx[kMaxBetween], page[kMaxBetween];
   unsigned long long key[kMaxBetween];
 };
 
-// Exact order key of one head's score in a page, by one warp; 0 (last) for a page outside the pool,
-// ~0 for a score that is no number (one such head makes the page rank last).
-template <typename T, typename K>
-__device__ __forceinline__ unsigned long long exact_key(const SelectPagesArgs& a, const T* q, int seq, int g, int p) {
+// Exact order keys of pages [0, m) of `page` (pool numbers, -1: 0, which ranks last): the greatest
+// head's, or 0 where one is no number.  Bounds go through shared memory, kExactPages at a time; eight
+// lanes take a (page, head).
+template <typename T, typename K, int kT>
+__device__ void exact_keys(const SelectPagesArgs& a, const T* sq, uint4* stage, const int* page, int g, int m,
+                           unsigned long long* key) {
   const PagedView& kv = a.kv;
-  const int lane = threadIdx.x & 31;
-  const int64_t page = paged_page(kv, seq, p);
-  if (page < 0) {
-    if (lane == 0) paged_err(kv, RTP_PAGED_ERANGE);
-    return 0ull;
+  const int D = kv.D, tid = threadIdx.x, units = 2 * D * (int)sizeof(K) / 16;
+  for (int j0 = 0; j0 < m; j0 += kExactPages) {
+    const int n = min(kExactPages, m - j0);
+    __syncthreads();
+    for (int i = tid; i < n * units; i += kT) {
+      const int64_t p = page[j0 + i / units];
+      stage[i] = p < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                       : ((const uint4*)((const K*)kv.bounds + ((p * kv.Hkv + g) * 2) * D))[i % units];
+    }
+    for (int i = tid; i < n; i += kT) key[j0 + i] = 0ull;
+    __syncthreads();
+    const int l = tid & 7;
+    for (int j = tid >> 3; j < (n * a.group + 3) / 4 * 4; j += kT / 8) {  // whole warps
+      const bool live = j < n * a.group;
+      const int jp = live ? j / a.group : 0;
+      const K* lim = (const K*)stage + jp * 2 * D;
+      const T* q = sq + (live ? j % a.group : 0) * D;
+      double s = 0.0;
+      for (int d = l; d < D; d += 8) {
+        const double x = to_f32(q[d]);
+        s += x * (double)to_f32(x < 0.0 ? lim[d] : lim[D + d]);
+      }
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      s += __shfl_xor_sync(0xffffffffu, s, 4);
+      if (live && l == 0) atomicMax(&key[j0 + jp], s != s ? ~0ull : order_key64(s));
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kT)
+      if (key[j0 + i] == ~0ull || page[j0 + i] < 0) key[j0 + i] = 0ull;
   }
-  const K* lim = (const K*)kv.bounds + ((page * kv.Hkv + g) * 2) * kv.D;
-  double s = 0.0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int d = e * 32 + lane;
-    const double x = d < kv.D ? to_f32(q[d]) : 0.f;
-    const double lo = d < kv.D ? to_f32(lim[d]) : 0.f, hi = d < kv.D ? to_f32(lim[kv.D + d]) : 0.f;
-    s += x * (x < 0.0 ? lo : hi);
-  }
-  s = warp_sum(s);
-  return s != s ? ~0ull : order_key64(s);
+  __syncthreads();
 }
 
 // One CTA of kT threads per (KV head, row); the scores in shared memory, or in the workspace itself.
 template <typename T, typename K, int kT, bool kSmem>
 __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, int chunks) {
-  extern __shared__ float list_[];
+  extern __shared__ __align__(16) uint8_t dyn[];  // [kExactPages][2 D] bounds, [group][D] queries, [pages] scores
   __shared__ PickShared s;
   const PagedView& kv = a.kv;
   const int g = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint4* stage = reinterpret_cast<uint4*>(dyn);
+  T* sq = reinterpret_cast<T*>(dyn + kExactPages * 2 * kv.D * sizeof(K));
+  float* list = reinterpret_cast<float*>(sq + a.group * kv.D);
   for (int i = tid; i < kBins; i += kT) s.hist[i] = 0;
-  for (int i = tid; i < kMaxBetween; i += kT) s.key[i] = 0ull;
-  if (tid == 0) s.got = 0;
+  if (tid == 0) {
+    s.got = 0;
+    s.low = ~0u;
+    s.high = s.mag = s.q1 = 0u;
+  }
   // the operator's inputs may be read ahead of the scores, its outputs be written
   int seq;
   const int len = paged_row(kv, a.row_seq, a.row_len, r, &seq);
@@ -302,63 +357,62 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
   if (tid == 0) a.sel_count[prob] = take;
   for (int i = take + tid; i < a.top; i += kT) sel[i] = -1;
   float* ws = a.approx + prob * kv.max_pages;
-  float* x = kSmem ? list_ : ws;
-  const T* q = (const T*)a.q + r * a.q_stride + (int64_t)g * a.group * kv.D;
+  float* x = kSmem ? list : ws;
   // a page is in if its score lies in a bin from `cut` on, or is +inf
   float lo = 0.f, scale = 0.f;
   int cut = kBins;
   const auto bin_of = [&](float y) { return min(kBins - 1, (int)((y - lo) * scale)); };
   const bool choose = want > 0 && want < c1 - c0;
-  float q1 = 0.f;  // the greatest |q|_1 of the heads
-  if (choose)
+  __syncthreads();
+  if (choose) {
+    // the queries, and the greatest |q|_1 of the heads
+    const T* q = (const T*)a.q + r * a.q_stride + (int64_t)g * a.group * kv.D;
+    float q1 = 0.f;
     for (int u = warp; u < a.group; u += kT / 32) {
       float y = 0.f;
-      for (int d = lane; d < kv.D; d += 32) y += fabsf(to_f32(q[u * kv.D + d]));
+      for (int d = lane; d < kv.D; d += 32) {
+        const T v = q[u * kv.D + d];
+        sq[u * kv.D + d] = v;
+        y += fabsf(to_f32(v));
+      }
       q1 = fmaxf(q1, warp_sum(y));
     }
+    if (lane == 0) atomicMax(&s.q1, q1 != q1 ? 0x7f800000u : __float_as_uint(q1));
+  }
   after_wait();
   if (choose) {
     // the scores' range; eps
-    float low = INFINITY, high = -INFINITY, mag = 0.f;
+    uint32_t low = ~0u, high = 0u;
+    float mag = 0.f;
     bool odd = false;
 #pragma unroll 4
     for (int i = c0 + tid; i < c1; i += kT) {
       const float y = ws[i];
       if (kSmem) x[i] = y;
-      low = fminf(low, y);
-      high = fmaxf(high, y);
+      low = min(low, order_key(y));
+      high = max(high, order_key(y));
       odd |= !isfinite(y);
     }
     for (int i = tid; i < chunks && i * kPageChunk < pages; i += kT) mag = fmaxf(mag, a.chunk_max[prob * chunks + i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-      high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
-      mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, o));
-    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    const uint32_t mags = __reduce_max_sync(0xffffffffu, __float_as_uint(mag));
     if (lane == 0) {
-      s.f[0][warp] = low;
-      s.f[1][warp] = high;
-      s.f[2][warp] = mag;
-      s.f[3][warp] = q1;
+      atomicMin(&s.low, low);
+      atomicMax(&s.high, high);
+      atomicMax(&s.mag, mags);
     }
     odd = __syncthreads_or(odd);
-#pragma unroll
-    for (int w = 0; w < kT / 32; ++w) {
-      low = fminf(low, s.f[0][w]);
-      high = fmaxf(high, s.f[1][w]);
-      mag = fmaxf(mag, s.f[2][w]);
-      q1 = fmaxf(q1, s.f[3][w]);
-    }
+    const float least = key_to_float(s.low), range = key_to_float(s.high) - least;
     // 1.01 covers the rounding of |q|_1 and of this product; 2^-110 what underflows in fp32
-    const float eps = 1.01f * 6.103515625e-05f * q1 * mag + 7.7e-34f;
+    const float eps = 1.01f * 6.103515625e-05f * __uint_as_float(s.q1) * __uint_as_float(s.mag) + 7.7e-34f;
     // Bins at least 2.5 eps wide (a bin's place is off by less than 2^-12 of a bin): whatever lies
     // within 2 eps of the last page taken lies in its bin or a neighbouring one.
-    const float range = high - low;
     bool done = !odd && isfinite(eps) && isfinite(range);
     if (done) {
-      lo = low;
+      lo = least;
       scale = fminf((float)kBins / fmaxf(range, 1e-30f), 0.4f / eps);
+#pragma unroll 4
       for (int i = c0 + tid; i < c1; i += kT) atomicAdd(&s.hist[bin_of(x[i])], 1u);
       __syncthreads();
       constexpr int B = kBins / kT;
@@ -383,20 +437,16 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
     if (done) {
       const int bin = s.bin, m = s.n_between, need = want - s.n_in;
       cut = bin + 2;
+#pragma unroll 4
       for (int i = c0 + tid; i < c1; i += kT) {
         const int b = bin_of(x[i]);
-        if (b >= bin - 1 && b <= bin + 1) s.idx[atomicAdd(&s.got, 1)] = i;
+        if (b >= bin - 1 && b <= bin + 1) {
+          const int at = atomicAdd(&s.got, 1);
+          s.idx[at] = i;
+          s.page[at] = (int)paged_page(kv, seq, i);
+        }
       }
-      __syncthreads();
-      // a warp per page and head; the greatest head's key
-      for (int j = warp; j < m * a.group; j += kT / 32) {
-        const unsigned long long k = exact_key<T, K>(a, q + j % a.group * kv.D, seq, g, s.idx[j / a.group]);
-        if (lane == 0) atomicMax(&s.key[j / a.group], k);
-      }
-      __syncthreads();
-      for (int j = tid; j < m; j += kT)
-        if (s.key[j] == ~0ull) s.key[j] = 0ull;
-      __syncthreads();
+      exact_keys<T, K, kT>(a, sq, stage, s.page, g, m, s.key);
       for (int j = tid; j < m; j += kT) {
         const unsigned long long k = s.key[j];
         const int i = s.idx[j];
@@ -408,12 +458,16 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
     } else {
       // every page by its exact score
       unsigned long long* keys = a.keys + prob * kv.max_pages;
-      for (int i = c0 + warp; i < c1; i += kT / 32) {
-        unsigned long long k = 0ull;
-        for (int u = 0; u < a.group; ++u) k = max(k, exact_key<T, K>(a, q + u * kv.D, seq, g, i));
-        if (lane == 0) keys[i] = k == ~0ull ? 0ull : k;
+      for (int i0 = c0; i0 < c1; i0 += kMaxBetween) {
+        const int n = min(kMaxBetween, c1 - i0);
+        for (int i = tid; i < n; i += kT) {
+          s.page[i] = (int)paged_page(kv, seq, i0 + i);
+          if (s.page[i] < 0) paged_err(kv, RTP_PAGED_ERANGE);
+        }
+        exact_keys<T, K, kT>(a, sq, stage, s.page, g, n, s.key);
+        for (int i = tid; i < n; i += kT) keys[i0 + i] = s.key[i];
+        __syncthreads();
       }
-      __syncthreads();
       int ties;
       const unsigned long long kth = block_kth_largest(c1 - c0, want, s.small, &ties, [&](int i) { return keys[c0 + i]; });
       int tied = 0;
@@ -431,53 +485,62 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
       __syncthreads();
     }
   }
-  // the pages taken, ascending: a warp takes a contiguous piece
+  // The pages taken, ascending: a thread takes an odd number of successive pages (no bank conflicts),
+  // counts, and writes behind the threads before it.
   const bool all = want >= c1 - c0;
-  const int per = (pages + kT - 1) / kT * 32;
-  const int i0 = warp * per, i1 = min(pages, i0 + per);
   const auto taken = [&](int i) {
     if (i < c0 || i >= c1 || all) return true;
     if (want <= 0) return false;
     const float y = x[i];
     return y == INFINITY || bin_of(y) >= cut;
   };
-  int n = 0;
-  for (int i = i0 + lane; i - lane < i1; i += 32) n += __popc(__ballot_sync(0xffffffffu, i < i1 && taken(i)));
-  int total;
-  int at = block_exclusive(lane == 0 ? n : 0, s.sums, &total);
-  at = __shfl_sync(0xffffffffu, at, 0);
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const bool in = i < i1 && taken(i);
-    const uint32_t bits = __ballot_sync(0xffffffffu, in);
-    if (in) sel[at + __popc(bits & ((1u << lane) - 1u))] = i;
-    at += __popc(bits);
+  const int per = (pages + kT - 1) / kT | 1;
+  const int i0 = min(pages, tid * per), i1 = min(pages, i0 + per);
+  int n = 0, total;
+  uint32_t verdict = 0;
+  for (int i = i0; i < i1; ++i) {
+    const bool in = taken(i);
+    if (i - i0 < kMaxPer) verdict |= (uint32_t)in << (i - i0);
+    n += in;
   }
+  int at = block_exclusive(n, s.sums, &total);
+  if (n)
+    for (int i = i0; i < i1; ++i)
+      if (i - i0 < kMaxPer ? (verdict >> (i - i0)) & 1u : taken(i)) sel[at++] = i;
 }
 
 template <typename T, typename K, int kT>
 cudaError_t run_pick(const SelectPagesArgs& a, int chunks, cudaStream_t st) {
   const dim3 grid(a.kv.Hkv, a.n_rows);
-  if (a.kv.max_pages > kPagesInSmem) return launch_after(page_pick_kernel<T, K, kT, false>, grid, kT, 0, st, a, chunks);
+  const size_t fixed = (size_t)kExactPages * 2 * a.kv.D * sizeof(K) + (size_t)a.group * a.kv.D * sizeof(T);
+  constexpr size_t kMost = kExactPages * 2 * kD * sizeof(T) + 64 * kD * sizeof(T);  // of `fixed`
+  cudaError_t e;
+  if (a.kv.max_pages > kPagesInSmem) {
+    static std::atomic<uint64_t> done{0};
+    if ((e = allow_smem(page_pick_kernel<T, K, kT, false>, kMost, done)) != cudaSuccess) return e;
+    return launch_after(page_pick_kernel<T, K, kT, false>, grid, kT, fixed, st, a, chunks);
+  }
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(page_pick_kernel<T, K, kT, true>, kPagesInSmem * sizeof(float), done);
-  if (e != cudaSuccess) return e;
-  return launch_after(page_pick_kernel<T, K, kT, true>, grid, kT, a.kv.max_pages * sizeof(float), st, a, chunks);
+  if ((e = allow_smem(page_pick_kernel<T, K, kT, true>, kMost + kPagesInSmem * sizeof(float), done)) != cudaSuccess) return e;
+  return launch_after(page_pick_kernel<T, K, kT, true>, grid, kT, fixed + a.kv.max_pages * sizeof(float), st, a, chunks);
 }
 
 template <typename T, typename K, int D>
 cudaError_t run_select(const SelectPagesArgs& a, cudaStream_t st) {
   const int chunks = page_chunks(a.kv.max_pages);
-  const int row_block = a.row_seq ? kRowBlock : 1;
-  int m_pad = (row_block * a.group + 15) / 16 * 16;
-  if (m_pad > kMaxM) m_pad = kMaxM;
-  constexpr int QS = 2 * D + 16;
-  const size_t smem = (size_t)2 * m_pad * QS + (size_t)row_block * kPageChunk * sizeof(uint32_t);
+  int row_block = a.row_seq ? kRowBlock : 1;
+  while (row_block * a.group > kMaxM) row_block /= 2;
+  const int m_pad = (row_block * a.group + 15) / 16 * 16;
+  // as many pages per CTA as still leaves two CTAs for every SM: the queries are laid out once for them
+  const int blocks = (a.n_rows + row_block - 1) / row_block, groups = (chunks + kScoreWarps - 1) / kScoreWarps;
+  int rounds = groups;
+  while (rounds > 1 && (int64_t)((groups + rounds - 1) / rounds) * a.kv.Hkv * blocks < 2 * 148) rounds = (rounds + 1) / 2;
+  using S = Score<T, K, D>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(page_score_kernel<T, K, D>, (size_t)2 * kMaxM * QS + kRowBlock * kPageChunk * sizeof(uint32_t),
-                             done);
+  cudaError_t e = allow_smem(page_score_kernel<T, K, D>, S::smem(kMaxM, kRowBlock), done);
   if (e != cudaSuccess) return e;
-  e = launch_after(page_score_kernel<T, K, D>, dim3(chunks, a.kv.Hkv, (a.n_rows + row_block - 1) / row_block),
-                   32 * kScoreWarps, smem, st, a, row_block, m_pad);
+  e = launch_after(page_score_kernel<T, K, D>, dim3((groups + rounds - 1) / rounds, a.kv.Hkv, blocks), 32 * kScoreWarps,
+                   S::smem(m_pad, row_block), st, a, row_block, m_pad, rounds, chunks);
   if (e != cudaSuccess) return e;
   // Few lists: as many threads as a CTA has, for the latency; many: small CTAs, many at once.
   const int64_t lists = (int64_t)a.n_rows * a.kv.Hkv;

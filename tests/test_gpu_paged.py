@@ -641,3 +641,19 @@ def test_decode_many_ragged_rows():
     lens = np.where(r.random(700) < 0.3, 0, r.integers(1, 60, 700))
     lens[123], lens[699] = 9000, 3000
     run_decode(Case(lens.tolist(), hq=3, hkv=1, d=64, page=16, kv="fp16", seed=16))
+
+
+@pytest.mark.parametrize("group", [1, 5, 8, 16, 64])
+def test_select_chunk_rows(group):
+    """Runs of rows of one sequence inside and across the blocks that share a read of the bounds;
+    groups whose heads are laid out in several goes."""
+    c = Case([1300, 700, 2500], hq=group, hkv=1, d=64, page=16, kv="fp16", seed=group)
+    bounds = torch.from_numpy(stored_bounds(c)).float().to(c.kt).to(c.device)
+    seq = [0] * 3 + [1] * 9 + [0] * 2 + [2] * 20 + [1]
+    r = np.random.default_rng(group)
+    n = [int(r.integers(0, c.lens[b] + 1)) for b in seq]
+    x = c.randn(len(seq), group, 64).to(c.qt).to(c.device)
+    sel, cnt = c.cache(bounds=bounds).select_pages(x, c.ints(n), 12, row_seq=c.ints(seq), n_first=1, n_recent=1)
+    for i, b in enumerate(seq):
+        want = page_choice(c, f64(bounds), f64(x)[i], b, n[i], 0, 12, 1, 1)
+        assert sel[i, 0].tolist() == want + [-1] * (12 - len(want)) and int(cnt[i, 0]) == len(want)
