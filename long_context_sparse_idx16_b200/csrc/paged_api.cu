@@ -63,6 +63,20 @@ const char* view_of(const rtp_paged_kv* kv, PagedView* p) {
   return nullptr;
 }
 
+// rope_base^(-2c/D) for c < D/2.  64 calls of pow take 2 us, as long as a launch: the last table of a
+// thread is kept with the numbers it was made from.
+void frequencies(double base, int D, double* theta) {
+  thread_local double table[kD / 2];
+  thread_local double of_base = 0.0;
+  thread_local int of_D = 0;
+  if (base != of_base || D != of_D) {
+    for (int c = 0; c < D / 2; ++c) table[c] = pow(base, -2.0 * c / D);
+    of_base = base;
+    of_D = D;
+  }
+  for (int c = 0; c < D / 2; ++c) theta[c] = table[c];
+}
+
 const char* check_io_dtype(const rtp_paged_kv* kv, int dtype) {
   if (dtype != RTP_FP16 && dtype != RTP_BF16) return "activations must be fp16 or bf16";
   if (kv->dtype != RTP_E4M3 && kv->dtype != dtype) return "activations must have the pages' dtype";
@@ -133,7 +147,7 @@ rtp_status rtp_paged_append(const rtp_paged_kv* kv, const void* q, const void* k
   a.q_out_stride = q_out_stride;
   a.slot_pos = slot_pos;
   a.slot_pos_stride = slot_pos_stride;
-  for (int c = 0; c < D / 2; ++c) a.theta[c] = pow(rope_base, -2.0 * c / D);
+  frequencies(rope_base, D, a.theta);
   const cudaError_t e = launch_paged_append(a, dtype, kv->dtype, stream);
   return e == cudaSuccess ? RTP_OK : cuda_fail(nullptr, e, fn);
 }

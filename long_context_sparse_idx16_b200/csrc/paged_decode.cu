@@ -58,6 +58,7 @@ struct AttnArgs {
   int octets;            // 8 * octets query heads per problem: 1 or 2
   int blocks;            // problems per KV head
   int box;               // slots per TMA box: min(page_size, 64)
+  int whole;             // problems are never split (short caches)
   int n_entries, mult;   // dense: rows, Hkv * blocks; page lists: rows * Hkv, blocks
   int64_t* prefix;       // [n_entries + 1] tiles (with overhead) of the entries before, one problem each
   float* lse2;           // [rows][Hq] base-2 log-sum-exp, or NULL
@@ -102,8 +103,10 @@ __device__ __forceinline__ Entry entry_of(const AttnArgs& a, int e) {
   return n;
 }
 
-// Length of an entry's problem in the numbering: its tiles and the overhead.
-__device__ __forceinline__ int64_t units_of(const Entry& n) { return n.tiles ? n.tiles + kOverhead : 0; }
+// Length of an entry's problem in the numbering: its tiles and the overhead (1 if it is not to be split).
+__device__ __forceinline__ int64_t units_of(const AttnArgs& a, const Entry& n) {
+  return !n.tiles ? 0 : a.whole ? 1 : n.tiles + kOverhead;
+}
 
 // First number of CTA c's range.
 __device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) { return total * c / ctas; }
@@ -147,7 +150,7 @@ __device__ __forceinline__ void tile_prefix(const AttnArgs& a, int64_t* out, int
   int64_t run = 0;
   for (int e0 = 0; e0 < a.n_entries; e0 += 32) {
     const int e = e0 + lane;
-    const int64_t t = e < a.n_entries ? units_of(entry_of(a, e)) : 0;
+    const int64_t t = e < a.n_entries ? units_of(a, entry_of(a, e)) : 0;
     int64_t y = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnArgs a) {
     const int e = e0 + tid * kPlan;
     int64_t t[kPlan], own = 0;
 #pragma unroll
-    for (int u = 0; u < kPlan; ++u) t[u] = e + u < a.n_entries ? units_of(entry_of(a, e + u)) : 0;
+    for (int u = 0; u < kPlan; ++u) t[u] = e + u < a.n_entries ? units_of(a, entry_of(a, e + u)) : 0;
 #pragma unroll
     for (int u = 0; u < kPlan; ++u) own += t[u];
     int64_t y = own;
@@ -223,10 +226,15 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& a, const int64_t* 
   }
   s.e = lo;
   s.n = entry_of(a, lo);
-  const int64_t x = t - prefix[lo] * a.mult, u = units_of(s.n);
+  const int64_t x = t - prefix[lo] * a.mult, u = units_of(a, s.n);
   s.prob = (int)(x / u);
   const int64_t at = x - s.prob * u;
   s.units = min(u - at, t1 - t);
+  if (a.whole) {
+    s.first = 0;
+    s.count = s.n.tiles;
+    return s;
+  }
   // the overhead comes first
   s.first = (int)max(at - kOverhead, (int64_t)0);
   s.count = (int)max(at + s.units - kOverhead - s.first, (int64_t)0);
@@ -288,26 +296,21 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
   const uint32_t job_full = smem_u32(&sh.job_full), job_empty = smem_u32(&sh.job_empty), meet = smem_u32(&sh.meet);
   volatile int* stop = &sh.stop;
   const bool inl = a.n_entries <= kInline;
-  if (tid == 0) {
+  if (tid == 32 * kConsumers) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&km) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&vm) : "memory");
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, kConsumers);
+    }
+    mbar_init(job_full, 1);
+    mbar_init(job_empty, kConsumers);
+    mbar_init(meet, kConsumers);
+    fence_mbar_init();
+    sh.stop = 0;
   }
   after_wait();
-  if (warp == kConsumers) {
-    if (lane == 0) {
-      for (int i = 0; i < ST; ++i) {
-        mbar_init(full + 8 * i, 1);
-        mbar_init(empty + 8 * i, kConsumers);
-      }
-      mbar_init(job_full, 1);
-      mbar_init(job_empty, kConsumers);
-      mbar_init(meet, kConsumers);
-      fence_mbar_init();
-      sh.stop = 0;
-    }
-  } else if (warp == 0) {
-    if (inl) tile_prefix(a, sh.prefix, lane);
-  }
+  if (warp == 0 && inl) tile_prefix(a, sh.prefix, lane);
   __syncthreads();
   const int64_t* prefix = inl ? sh.prefix : a.prefix;
   const int64_t total = prefix[a.n_entries] * a.mult;
@@ -895,6 +898,9 @@ bool map_pages(CUtensorMap* m, void* base, const int64_t* stride, const rtp_page
                     bx, bytes < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Slots that a problem can have.
+int64_t slots_of(const AttnArgs& a) { return a.d.sel ? a.d.sel_stride * a.d.kv.page_size : a.cap; }
+
 template <typename QT, typename K, int D, int NB>
 cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   using S = Stage<K, D>;
@@ -903,19 +909,19 @@ cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(attn_kernel<QT, K, D, NB>, smem, done);
   if (e != cudaSuccess) return e;
-  const int64_t slots = a.d.sel ? a.d.sel_stride * a.d.kv.page_size : a.cap;
-  const int64_t most = (int64_t)a.n_entries * a.mult * ((slots + kTile - 1) / kTile + kOverhead);
+  const int64_t most = (int64_t)a.n_entries * a.mult * (a.whole ? 1 : slots_of(a) / kTile + 1 + kOverhead);
   const int sms = device_sms();
   int64_t grid = (int64_t)per_sm(NB) * (sms < kMaxSms ? sms : kMaxSms);
   if (grid > most) grid = most;
   if (a.n_entries > kInline && (e = launch_after(plan_kernel, dim3(1), 1024, 0, st, a)) != cudaSuccess) return e;
-  // Not launch_after: CTAs of the kernel before it, still waiting on an SM, would keep one of this
-  // kernel's CTAs from fitting there, and the grid is as large as the GPU (332 -> 406 us at 8 x 128K).
-  attn_kernel<QT, K, D, NB><<<(unsigned)grid, kThreads, smem, st>>>(a, km, vm);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const float bias = std::is_same_v<K, __nv_bfloat16> ? 0.f : 15.f;
-  e = launch_after(join_kernel<QT, D>, dim3((unsigned)grid, 8 * NB), kJoinWarps * 32, 0, st, a, bias);
-  if (e != cudaSuccess || !a.logits) return e;
+  e = launch_after(attn_kernel<QT, K, D, NB>, dim3((unsigned)grid), kThreads, smem, st, a, km, vm);
+  if (e != cudaSuccess) return e;
+  if (!a.whole) {
+    const float bias = std::is_same_v<K, __nv_bfloat16> ? 0.f : 15.f;
+    e = launch_after(join_kernel<QT, D>, dim3((unsigned)grid, 8 * NB), kJoinWarps * 32, 0, st, a, bias);
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.logits) return cudaSuccess;
   const int64_t blocks = (a.cap + 1023) / 1024;
   return launch_after(weights_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024), a.d.kv.Hkv, a.d.n_rows), 256, 0,
                       st, a);
@@ -943,6 +949,8 @@ cudaError_t launch_paged_decode(const DecodeArgs& d, const rtp_paged_kv* kv, int
   a.n_entries = d.sel ? d.n_rows * kv->n_kv_heads : d.n_rows;
   a.mult = d.sel ? a.blocks : kv->n_kv_heads * a.blocks;
   a.cap = (int64_t)kv->max_pages * kv->page_size;
+  // Four tiles take less time in one CTA than a second launch to join them does.
+  a.whole = slots_of(a) <= 4 * kTile;
   const Layout l = layout_of(kv, d.n_rows, d.Hq, d.scores != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(d.workspace);
   a.prefix = reinterpret_cast<int64_t*>(ws + l.prefix);
