@@ -29,7 +29,7 @@
 //     output rows.  Their queries are scaled per head by a power of two into fp16's range, which is
 //     exact for values down to 2^-29 of the head's largest and off by 2^-40 of that below.
 // Accumulated weights need the final log-sum-exp: the scores go through the workspace in fp32 and
-// weights_kernel adds exp(s - lse) over the query heads.
+// weights_kernel adds exp(s - lse) over the query heads, beside the join.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -66,6 +66,7 @@ struct AttnArgs {
   int64_t cap;
   int4* split;           // [CTAs] problem that the CTA begins and others go on with: (row, query head,
                          // heads, last CTA), or row -1
+  int2* span;            // [rows][Hkv * blocks] first and last CTA of a split problem, or -1 (with logits)
   float2* part_ml;       // [CTAs][continued, begun][16]
   float* part_o;         // [CTAs][continued, begun][16][D]
 };
@@ -367,12 +368,16 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
         j.whole = s.count == s.n.tiles;
         j.last = t >= t1;
         mbar_expect_tx(job_full, s.count ? nh * 2 * D : 0);
-        if (s.count && s.first == 0 && s.count < s.n.tiles) {
-          // the CTA with the problem's last tile
-          const int64_t end = t + (s.n.tiles - s.count) - 1;
-          int c1 = (int)(end * ctas / total);
-          while (c1 + 1 < ctas && range_start(total, c1 + 1, ctas) <= end) ++c1;
-          a.split[blockIdx.x] = make_int4(s.n.row, g * d.group + h0, nh, c1);
+        if (s.count && s.first == 0) {  // a problem begins here
+          int c1 = -1;
+          if (s.count < s.n.tiles) {
+            // the CTA with its last tile
+            const int64_t end = t + (s.n.tiles - s.count) - 1;
+            c1 = (int)(end * ctas / total);
+            while (c1 + 1 < ctas && range_start(total, c1 + 1, ctas) <= end) ++c1;
+            a.split[blockIdx.x] = make_int4(s.n.row, g * d.group + h0, nh, c1);
+          }
+          if (a.logits) a.span[(int64_t)s.n.row * a.mult + s.prob] = make_int2(c1 < 0 ? -1 : (int)blockIdx.x, c1);
         }
       }
       __syncwarp();
@@ -746,14 +751,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
 constexpr int kJoinWarps = 8;
 
 template <typename QT, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a, float bias) {
+__device__ void join_part(const AttnArgs& a, float bias, int c0, int hrow) {
   const DecodeArgs& d = a.d;
   const PagedView& kv = d.kv;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c0 = blockIdx.x, hrow = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ float weight[kMaxPerSm * kMaxSms];
   __shared__ float red[2][kJoinWarps];
   __shared__ float so[kJoinWarps][D];
-  after_wait();
   const int4 s = a.split[c0];
   if (s.x < 0 || hrow >= s.z) return;
   const int r = s.x, h = s.y + hrow, n = s.w - c0 + 1;
@@ -824,32 +828,65 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
   if (tid == 0) {
     const float y = L == 0.f ? -INFINITY : M + (log2f(L) - bias);
     if (d.lse) d.lse[at] = y * 0.6931471805599453f;
-    if (a.lse2) a.lse2[at] = y;
   }
 }
 
-// scores[row][g][j] += sum over g's heads of exp2(logit - lse2), for the slots attended.
-__global__ void __launch_bounds__(256) weights_kernel(const AttnArgs a) {
+// scores[row][g][j] += sum over g's heads of exp2(logit - lse2), for the slots attended.  The
+// log-sum-exp of a split problem is joined here again, a warp per head.
+__device__ void add_weights(const AttnArgs& a, float bias, int chunk, int chunks) {
   const DecodeArgs& d = a.d;
   const PagedView& kv = d.kv;
-  const int g = blockIdx.y, r = blockIdx.z;
+  const int g = blockIdx.y, r = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ float lse[64];
   const Entry n = entry_of(a, r);
-  after_wait();
-  if (threadIdx.x < d.group) {
-    const float y = a.lse2[(int64_t)r * d.Hq + g * d.group + threadIdx.x];
-    lse[threadIdx.x] = y == -INFINITY ? INFINITY : y;
+  const int slots = n.sinks + n.len - n.lo;
+  if (chunk * (kJoinWarps * 32) >= slots) return;
+  const int heads = 8 * a.octets;
+  for (int u = warp; u < d.group; u += kJoinWarps) {
+    const int2 c = a.span[(int64_t)r * a.mult + g * a.blocks + u / heads];
+    float y;
+    if (c.x < 0) {
+      y = a.lse2[(int64_t)r * d.Hq + g * d.group + u];
+    } else {
+      float m = -INFINITY, l = 0.f;
+      for (int i = c.x + lane; i <= c.y; i += 32) {
+        const float2 p = a.part_ml[(2 * (int64_t)i + (i == c.x ? 1 : 0)) * 16 + u % heads];
+        const float mn = fmaxf(m, p.x), base = mn == -INFINITY ? 0.f : mn;
+        l = l * exp2f(m - base) + p.y * exp2f(p.x - base);
+        m = mn;
+      }
+      const float M = warp_max(m);
+      const float L = warp_sum(l * exp2f(m - (M == -INFINITY ? 0.f : M)));
+      y = L == 0.f ? -INFINITY : M + (log2f(L) - bias);
+    }
+    if (lane == 0) lse[u] = y == -INFINITY ? INFINITY : y;
   }
   __syncthreads();
   const float* lg = a.logits + ((int64_t)r * d.Hq + g * d.group) * a.cap;
   float* sc = d.scores + ((int64_t)r * kv.Hkv + g) * d.scores_stride;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < n.sinks + n.len - n.lo; i += gridDim.x * 256) {
+  for (int i = chunk * (kJoinWarps * 32) + threadIdx.x; i < slots; i += chunks * (kJoinWarps * 32)) {
     const int j = i < n.sinks ? i : n.lo + i - n.sinks;
     if (paged_page(kv, n.seq, j >> kv.page_shift) < 0) continue;
     float w = 0.f;
+#pragma unroll 8
     for (int u = 0; u < d.group; ++u) w += fast_exp2(lg[u * a.cap + j] - lse[u]);
     sc[j] += w;
   }
+}
+
+// The join, and with accumulated weights also these: both need only what attn_kernel left.
+template <typename QT, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a, float bias, int heads) {
+  after_wait();
+  join_part<QT, D>(a, bias, blockIdx.x / heads, blockIdx.x % heads);
+}
+template <typename QT, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) weights_kernel(const AttnArgs a, float bias, int heads, int joins,
+                                                                  int chunks) {
+  after_wait();
+  if ((int)blockIdx.x < chunks) return add_weights(a, bias, blockIdx.x, chunks);
+  const int64_t i = ((int64_t)(blockIdx.x - chunks) * gridDim.z + blockIdx.z) * gridDim.y + blockIdx.y;
+  if (i < joins) join_part<QT, D>(a, bias, (int)i / heads, (int)i % heads);
 }
 
 // ---- host
@@ -867,7 +904,7 @@ int device_sms() {
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Layout {
-  size_t prefix, split, lse2, ml, o, logits, total;
+  size_t prefix, split, span, lse2, ml, o, logits, total;
 };
 Layout layout_of(const rtp_paged_kv* kv, int n_rows, int n_q_heads, bool scores) {
   Layout l;
@@ -882,6 +919,8 @@ Layout layout_of(const rtp_paged_kv* kv, int n_rows, int n_q_heads, bool scores)
   l.split = take((size_t)kMaxPerSm * kMaxSms * sizeof(int4));
   l.ml = take(parts * sizeof(float2));
   l.o = take(parts * kv->head_dim * sizeof(float));
+  const int group = n_q_heads / kv->n_kv_heads, blocks = group <= 8 ? 1 : (group + 15) / 16;
+  l.span = take(scores ? (size_t)n_rows * kv->n_kv_heads * blocks * sizeof(int2) : 0);
   l.lse2 = take(scores ? (size_t)n_rows * n_q_heads * sizeof(float) : 0);
   l.logits = take(scores ? (size_t)n_rows * n_q_heads * kv->max_pages * kv->page_size * sizeof(float) : 0);
   l.total = at;
@@ -916,15 +955,14 @@ cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
   if (a.n_entries > kInline && (e = launch_after(plan_kernel, dim3(1), 1024, 0, st, a)) != cudaSuccess) return e;
   e = launch_after(attn_kernel<QT, K, D, NB>, dim3((unsigned)grid), kThreads, smem, st, a, km, vm);
   if (e != cudaSuccess) return e;
-  if (!a.whole) {
-    const float bias = std::is_same_v<K, __nv_bfloat16> ? 0.f : 15.f;
-    e = launch_after(join_kernel<QT, D>, dim3((unsigned)grid, 8 * NB), kJoinWarps * 32, 0, st, a, bias);
-    if (e != cudaSuccess) return e;
-  }
-  if (!a.logits) return cudaSuccess;
-  const int64_t blocks = (a.cap + 1023) / 1024;
-  return launch_after(weights_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024), a.d.kv.Hkv, a.d.n_rows), 256, 0,
-                      st, a);
+  const float bias = std::is_same_v<K, __nv_bfloat16> ? 0.f : 15.f;
+  const int joins = a.whole ? 0 : (int)grid * 8 * NB;
+  if (!a.logits)
+    return joins ? launch_after(join_kernel<QT, D>, dim3(joins), kJoinWarps * 32, 0, st, a, bias, 8 * NB) : cudaSuccess;
+  const int64_t chunks = (a.cap + 1023) / 1024, lists = (int64_t)a.d.kv.Hkv * a.d.n_rows;
+  const int blocks = (int)(chunks < 1024 ? chunks : 1024);
+  return launch_after(weights_kernel<QT, D>, dim3((unsigned)(blocks + (joins + lists - 1) / lists), a.d.kv.Hkv, a.d.n_rows),
+                      kJoinWarps * 32, 0, st, a, bias, 8 * NB, joins, blocks);
 }
 
 template <typename QT, typename K>
@@ -958,6 +996,7 @@ cudaError_t launch_paged_decode(const DecodeArgs& d, const rtp_paged_kv* kv, int
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   a.part_o = reinterpret_cast<float*>(ws + l.o);
   if (d.scores) {
+    a.span = reinterpret_cast<int2*>(ws + l.span);
     a.lse2 = reinterpret_cast<float*>(ws + l.lse2);
     a.logits = reinterpret_cast<float*>(ws + l.logits);
   }

@@ -166,12 +166,23 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
       nh += !in && i < keep;
     }
     int holes;
-    int om = block_exclusive(nm, s.a, &moved);
-    int oh = block_exclusive(nh, s.b, &holes);
+    int om, oh;
+    if (kSmem) {  // both counts in one sum: they stay below 2^16
+      const int both = block_exclusive(nm | nh << 16, s.a, &holes);
+      om = both & 0xffff;
+      oh = both >> 16;
+      moved = holes & 0xffff;
+    } else {
+      om = block_exclusive(nm, s.a, &moved);
+      oh = block_exclusive(nh, s.b, &holes);
+    }
+    // the keys have served: their place takes the lists (moved <= n / 2)
+    int32_t* movers = kSmem ? reinterpret_cast<int32_t*>(keys) : mover;
+    int32_t* freed = kSmem ? movers + moved : hole;
     for (int i = i0; i < i1; ++i) {
       const bool in = kSmem ? (verdict >> (i - i0)) & 1u : stays(i);
-      if (in && i >= keep) mover[om++] = i;
-      if (!in && i < keep) hole[oh++] = i;
+      if (in && i >= keep) movers[om++] = i;
+      if (!in && i < keep) freed[oh++] = i;
     }
     __syncthreads();
     // what moves in: the sources lie at or behind the budget, where nothing has been written yet
@@ -182,17 +193,22 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(const EvictArgs a) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int m = m0 + u * kThreads;
-        to[u] = m < moved ? hole[m] : 0;
-        from[u] = m < moved ? mover[m] : 0;
+        to[u] = m < moved ? freed[m] : 0;
+        from[u] = m < moved ? movers[m] : 0;
+        x[u] = sc[from[u]];
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) x[u] = sc[from[u]];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (m0 + u * kThreads < moved) {
+      for (int u = 0; u < kBatch; ++u) {
+        const int m = m0 + u * kThreads;
+        if (m < moved) {
+          if (kSmem) {
+            mover[m] = from[u];
+            hole[m] = to[u];
+          }
           a.out_scores[base + to[u]] = x[u];
           a.out_positions[base + to[u]] = position(from[u]);
         }
+      }
     }
     __syncthreads();
   }

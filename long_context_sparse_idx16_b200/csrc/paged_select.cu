@@ -275,7 +275,7 @@ constexpr int kMaxBetween = 256;  // pages ranked by their exact scores in share
 constexpr int kPagesInSmem = 40 * 1024;
 
 constexpr int kExactPages = 16;   // pages whose bounds are staged at a time for their exact scores
-constexpr int kMaxPer = 25;       // pages a thread keeps its verdicts of
+constexpr int kMaxPer = 64;       // pages a thread keeps its verdicts of
 
 struct PickShared {
   uint32_t hist[kBins];
@@ -288,13 +288,13 @@ struct PickShared {
 };
 
 // Exact order keys of pages [0, m) of `page` (pool numbers, -1: 0, which ranks last): the greatest
-// head's, or 0 where one is no number.  Bounds go through shared memory, kExactPages at a time; eight
-// lanes take a (page, head).
+// head's, or 0 where one is no number.  Bounds go through shared memory, kExactPages at a time; a warp
+// takes a (page, head).
 template <typename T, typename K, int kT>
-__device__ void exact_keys(const SelectPagesArgs& a, const T* sq, uint4* stage, const int* page, int g, int m,
-                           unsigned long long* key) {
+__device__ void exact_keys(const SelectPagesArgs& a, const T* sq, uint4* stage, unsigned long long* head_key,
+                           const int* page, int g, int m, unsigned long long* key) {
   const PagedView& kv = a.kv;
-  const int D = kv.D, tid = threadIdx.x, units = 2 * D * (int)sizeof(K) / 16;
+  const int D = kv.D, tid = threadIdx.x, lane = tid & 31, units = 2 * D * (int)sizeof(K) / 16;
   for (int j0 = 0; j0 < m; j0 += kExactPages) {
     const int n = min(kExactPages, m - j0);
     __syncthreads();
@@ -303,27 +303,28 @@ __device__ void exact_keys(const SelectPagesArgs& a, const T* sq, uint4* stage, 
       stage[i] = p < 0 ? make_uint4(0u, 0u, 0u, 0u)
                        : ((const uint4*)((const K*)kv.bounds + ((p * kv.Hkv + g) * 2) * D))[i % units];
     }
-    for (int i = tid; i < n; i += kT) key[j0 + i] = 0ull;
     __syncthreads();
-    const int l = tid & 7;
-    for (int j = tid >> 3; j < (n * a.group + 3) / 4 * 4; j += kT / 8) {  // whole warps
-      const bool live = j < n * a.group;
-      const int jp = live ? j / a.group : 0;
-      const K* lim = (const K*)stage + jp * 2 * D;
-      const T* q = sq + (live ? j % a.group : 0) * D;
+    for (int j = tid >> 5; j < n * a.group; j += kT / 32) {
+      const K* lim = (const K*)stage + j / a.group * 2 * D;
+      const T* q = sq + j % a.group * D;
       double s = 0.0;
-      for (int d = l; d < D; d += 8) {
-        const double x = to_f32(q[d]);
-        s += x * (double)to_f32(x < 0.0 ? lim[d] : lim[D + d]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = e * 32 + lane;
+        if (d < D) {
+          const float x = to_f32(q[d]), b = to_f32(x < 0.f ? lim[d] : lim[D + d]);
+          s += (double)x * (double)b;
+        }
       }
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      s += __shfl_xor_sync(0xffffffffu, s, 4);
-      if (live && l == 0) atomicMax(&key[j0 + jp], s != s ? ~0ull : order_key64(s));
+      s = warp_sum(s);
+      if (lane == 0) head_key[j] = s != s ? ~0ull : order_key64(s);
     }
     __syncthreads();
-    for (int i = tid; i < n; i += kT)
-      if (key[j0 + i] == ~0ull || page[j0 + i] < 0) key[j0 + i] = 0ull;
+    for (int i = tid; i < n; i += kT) {
+      unsigned long long k = 0ull;
+      for (int u = 0; u < a.group; ++u) k = max(k, head_key[i * a.group + u]);
+      key[j0 + i] = k == ~0ull || page[j0 + i] < 0 ? 0ull : k;
+    }
   }
   __syncthreads();
 }
@@ -331,12 +332,14 @@ __device__ void exact_keys(const SelectPagesArgs& a, const T* sq, uint4* stage, 
 // One CTA of kT threads per (KV head, row); the scores in shared memory, or in the workspace itself.
 template <typename T, typename K, int kT, bool kSmem>
 __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, int chunks) {
-  extern __shared__ __align__(16) uint8_t dyn[];  // [kExactPages][2 D] bounds, [group][D] queries, [pages] scores
+  // [kExactPages][2 D] bounds, [kExactPages][group] keys, [group][D] queries, [pages] scores
+  extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ PickShared s;
   const PagedView& kv = a.kv;
   const int g = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint4* stage = reinterpret_cast<uint4*>(dyn);
-  T* sq = reinterpret_cast<T*>(dyn + kExactPages * 2 * kv.D * sizeof(K));
+  unsigned long long* head_key = reinterpret_cast<unsigned long long*>(dyn + kExactPages * 2 * kv.D * sizeof(K));
+  T* sq = reinterpret_cast<T*>(head_key + kExactPages * a.group);
   float* list = reinterpret_cast<float*>(sq + a.group * kv.D);
   for (int i = tid; i < kBins; i += kT) s.hist[i] = 0;
   if (tid == 0) {
@@ -361,8 +364,13 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
   // a page is in if its score lies in a bin from `cut` on, or is +inf
   float lo = 0.f, scale = 0.f;
   int cut = kBins;
+  bool told = false;  // by the histogram and the exact scores of a few pages
   const auto bin_of = [&](float y) { return min(kBins - 1, (int)((y - lo) * scale)); };
   const bool choose = want > 0 && want < c1 - c0;
+  // a thread's own pages for the list at the end: an odd number of successive ones (no bank conflicts)
+  const int per = (pages + kT - 1) / kT | 1;
+  const int i0 = min(pages, tid * per), i1 = min(pages, i0 + per);
+  unsigned long long sure = 0ull, maybe = 0ull;  // of these pages: taken; to be told by their exact scores
   __syncthreads();
   if (choose) {
     // the queries, and the greatest |q|_1 of the heads
@@ -435,18 +443,21 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
       done = s.n_between <= kMaxBetween;
     }
     if (done) {
+      told = true;
       const int bin = s.bin, m = s.n_between, need = want - s.n_in;
       cut = bin + 2;
-#pragma unroll 4
-      for (int i = c0 + tid; i < c1; i += kT) {
+      for (int i = max(i0, c0); i < min(i1, c1); ++i) {
         const int b = bin_of(x[i]);
-        if (b >= bin - 1 && b <= bin + 1) {
+        if (b >= cut) {
+          sure |= 1ull << ((i - i0) & 63);
+        } else if (b >= bin - 1) {
+          maybe |= 1ull << ((i - i0) & 63);
           const int at = atomicAdd(&s.got, 1);
           s.idx[at] = i;
           s.page[at] = (int)paged_page(kv, seq, i);
         }
       }
-      exact_keys<T, K, kT>(a, sq, stage, s.page, g, m, s.key);
+      exact_keys<T, K, kT>(a, sq, stage, head_key, s.page, g, m, s.key);
       for (int j = tid; j < m; j += kT) {
         const unsigned long long k = s.key[j];
         const int i = s.idx[j];
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
           s.page[i] = (int)paged_page(kv, seq, i0 + i);
           if (s.page[i] < 0) paged_err(kv, RTP_PAGED_ERANGE);
         }
-        exact_keys<T, K, kT>(a, sq, stage, s.page, g, n, s.key);
+        exact_keys<T, K, kT>(a, sq, stage, head_key, s.page, g, n, s.key);
         for (int i = tid; i < n; i += kT) keys[i0 + i] = s.key[i];
         __syncthreads();
       }
@@ -485,8 +496,7 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
       __syncthreads();
     }
   }
-  // The pages taken, ascending: a thread takes an odd number of successive pages (no bank conflicts),
-  // counts, and writes behind the threads before it.
+  // The pages taken, ascending: each thread counts its own and writes behind the threads before it.
   const bool all = want >= c1 - c0;
   const auto taken = [&](int i) {
     if (i < c0 || i >= c1 || all) return true;
@@ -494,26 +504,41 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
     const float y = x[i];
     return y == INFINITY || bin_of(y) >= cut;
   };
-  const int per = (pages + kT - 1) / kT | 1;
-  const int i0 = min(pages, tid * per), i1 = min(pages, i0 + per);
-  int n = 0, total;
-  uint32_t verdict = 0;
-  for (int i = i0; i < i1; ++i) {
-    const bool in = taken(i);
-    if (i - i0 < kMaxPer) verdict |= (uint32_t)in << (i - i0);
-    n += in;
+  const bool bits = per <= kMaxPer;
+  if (bits) {
+    if (told) {
+      for (unsigned long long b = maybe; b; b &= b - 1) {
+        const int u = __ffsll((long long)b) - 1;
+        if (x[i0 + u] == INFINITY) sure |= 1ull << u;
+      }
+    }
+    if (!choose || !told) {
+      for (int i = i0; i < i1; ++i)
+        if (taken(i)) sure |= 1ull << (i - i0);
+    } else {
+      for (int i = i0; i < min(i1, c0); ++i) sure |= 1ull << (i - i0);
+      for (int i = max(i0, c1); i < i1; ++i) sure |= 1ull << (i - i0);
+    }
   }
+  int n = 0, total;
+  if (bits) n = __popcll(sure);
+  else
+    for (int i = i0; i < i1; ++i) n += taken(i);
   int at = block_exclusive(n, s.sums, &total);
-  if (n)
+  if (bits) {
+    for (unsigned long long b = sure; b; b &= b - 1) sel[at++] = i0 + __ffsll((long long)b) - 1;
+  } else if (n) {
     for (int i = i0; i < i1; ++i)
-      if (i - i0 < kMaxPer ? (verdict >> (i - i0)) & 1u : taken(i)) sel[at++] = i;
+      if (taken(i)) sel[at++] = i;
+  }
 }
 
 template <typename T, typename K, int kT>
 cudaError_t run_pick(const SelectPagesArgs& a, int chunks, cudaStream_t st) {
   const dim3 grid(a.kv.Hkv, a.n_rows);
-  const size_t fixed = (size_t)kExactPages * 2 * a.kv.D * sizeof(K) + (size_t)a.group * a.kv.D * sizeof(T);
-  constexpr size_t kMost = kExactPages * 2 * kD * sizeof(T) + 64 * kD * sizeof(T);  // of `fixed`
+  const size_t fixed = (size_t)kExactPages * 2 * a.kv.D * sizeof(K) +
+                       (size_t)a.group * (kExactPages * sizeof(unsigned long long) + a.kv.D * sizeof(T));
+  constexpr size_t kMost = kExactPages * 2 * kD * sizeof(T) + 64 * (kExactPages * 8 + kD * sizeof(T));  // of `fixed`
   cudaError_t e;
   if (a.kv.max_pages > kPagesInSmem) {
     static std::atomic<uint64_t> done{0};
