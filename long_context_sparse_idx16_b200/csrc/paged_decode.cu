@@ -84,13 +84,13 @@ __device__ __forceinline__ Entry entry_of(const AttnArgs& a, int e) {
   const PagedView& kv = d.kv;
   Entry n;
   n.row = d.sel ? e / kv.Hkv : e;
+  const int listed = d.sel ? d.sel_count[e] : 0;  // in flight together with the length
   n.len = paged_row(kv, d.row_seq, d.row_len, n.row, &n.seq);
   n.lo = n.sinks = n.t_sink = n.t_skip = n.n_list = 0;
   n.list = nullptr;
   if (d.sel) {
-    const int c = d.sel_count[e];
     n.list = d.sel + (int64_t)e * d.sel_stride;
-    n.n_list = n.len == 0 || c < 0 ? 0 : c > d.sel_stride ? (int)d.sel_stride : c;
+    n.n_list = n.len == 0 || listed < 0 ? 0 : listed > d.sel_stride ? (int)d.sel_stride : listed;
     n.tiles = (int)((((int64_t)n.n_list << kv.page_shift) + kTile - 1) / kTile);
     return n;
   }
@@ -109,8 +109,26 @@ __device__ __forceinline__ int64_t units_of(const AttnArgs& a, const Entry& n) {
   return !n.tiles ? 0 : a.whole ? 1 : n.tiles + kOverhead;
 }
 
-// First number of CTA c's range.
-__device__ __forceinline__ int64_t range_start(int64_t total, int c, int ctas) { return total * c / ctas; }
+// x / y for x >= 0, y > 0: in 32 bits where both fit, which is nearly always and much faster.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return (int64_t)((uint32_t)x / (uint32_t)y);
+  return x / y;
+}
+
+// The numbers [0, total) shared out over CTAs: the first `more` of them take one more than the others.
+struct Ranges {
+  int64_t total, each, more;
+  int ctas;
+  __device__ Ranges(int64_t total_, int grid) : total(total_), ctas((int)min((int64_t)grid, total_)) {
+    each = ctas ? quotient(total, ctas) : 0;
+    more = total - each * ctas;
+  }
+  __device__ int64_t start(int c) const { return each * c + min((int64_t)c, more); }
+  __device__ int owner(int64_t t) const {
+    const int64_t big = more * (each + 1);
+    return (int)(t < big ? quotient(t, each + 1) : more + quotient(t - big, each));
+  }
+};
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
                                             uint32_t mbar) {
@@ -228,7 +246,7 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs& a, const int64_t* 
   s.e = lo;
   s.n = entry_of(a, lo);
   const int64_t x = t - prefix[lo] * a.mult, u = units_of(a, s.n);
-  s.prob = (int)(x / u);
+  s.prob = (int)quotient(x, u);
   const int64_t at = x - s.prob * u;
   s.units = min(u - at, t1 - t);
   if (a.whole) {
@@ -261,6 +279,7 @@ struct Shared {
   unsigned long long full[8], empty[8], job_full, job_empty, meet;
   int base[8][4];                        // first slot of each box of a stage
   int stop;                              // a wait gave up
+  int verdict;                           // of the consumers, on the job that begins
   Job job;
   int64_t prefix[kInline + 1];
 };
@@ -308,14 +327,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
     mbar_init(job_empty, kConsumers);
     mbar_init(meet, kConsumers);
     fence_mbar_init();
-    sh.stop = 0;
+    sh.stop = sh.verdict = 0;
   }
   after_wait();
   if (warp == 0 && inl) tile_prefix(a, sh.prefix, lane);
   __syncthreads();
   const int64_t* prefix = inl ? sh.prefix : a.prefix;
-  const int64_t total = prefix[a.n_entries] * a.mult;
-  const int ctas = (int)min((int64_t)gridDim.x, total);
+  const Ranges ranges(prefix[a.n_entries] * a.mult, gridDim.x);
   if (tid == 32 * kConsumers) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);  // the thread that may overwrite it
   // entries without a tile: zeros
   for (int e = blockIdx.x; e < a.n_entries; e += gridDim.x) {
@@ -330,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
       if (a.lse2) a.lse2[(int64_t)r * d.Hq + h + x] = -INFINITY;
     }
   }
-  if ((int)blockIdx.x >= ctas) return;
-  const int64_t t0 = range_start(total, blockIdx.x, ctas), t1 = range_start(total, blockIdx.x + 1, ctas);
+  if ((int)blockIdx.x >= ranges.ctas) return;
+  const int64_t t0 = ranges.start(blockIdx.x), t1 = ranges.start(blockIdx.x + 1);
 
   if (warp == kConsumers) {
     // ---- producer: lane (half, block, box) issues one TMA box of a tile
@@ -368,22 +386,19 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
         j.whole = s.count == s.n.tiles;
         j.last = t >= t1;
         mbar_expect_tx(job_full, s.count ? nh * 2 * D : 0);
-        if (s.count && s.first == 0) {  // a problem begins here
-          int c1 = -1;
-          if (s.count < s.n.tiles) {
-            // the CTA with its last tile
-            const int64_t end = t + (s.n.tiles - s.count) - 1;
-            c1 = (int)(end * ctas / total);
-            while (c1 + 1 < ctas && range_start(total, c1 + 1, ctas) <= end) ++c1;
-            a.split[blockIdx.x] = make_int4(s.n.row, g * d.group + h0, nh, c1);
-          }
-          if (a.logits) a.span[(int64_t)s.n.row * a.mult + s.prob] = make_int2(c1 < 0 ? -1 : (int)blockIdx.x, c1);
-        }
       }
       __syncwarp();
       if (lane < nh && s.count)
         bulk_load(smem_u32(sh.q[lane]),
                   (const uint16_t*)d.q + s.n.row * d.q_stride + (int64_t)(g * d.group + h0 + lane) * D, 2 * D, job_full);
+      if (lane == 0 && s.count && s.first == 0) {  // a problem begins here
+        int c1 = -1;
+        if (s.count < s.n.tiles) {
+          c1 = ranges.owner(t + (s.n.tiles - s.count) - 1);  // the CTA with its last tile
+          a.split[blockIdx.x] = make_int4(s.n.row, g * d.group + h0, nh, c1);
+        }
+        if (a.logits) a.span[(int64_t)s.n.row * a.mult + s.prob] = make_int2(c1 < 0 ? -1 : (int)blockIdx.x, c1);
+      }
       jphase ^= 1u;
       // One tile ahead in the page table, two in the list: the look-ups' latency passes while the
       // ring is full.
@@ -448,22 +463,33 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
 
   // ---- consumers
   const int r0 = warp * 16, row = lane >> 2, c2 = (lane & 3) * 2;
-  // a warp that gives up a wait sets `stop` and leaves; the others then run out of their own waits
-  const auto gave_up = [&]() {
+  // A warp that gives up a wait sets `stop` and goes on without computing.  When a job begins the four
+  // warps meet (with a bounded wait) and the first to come out says whether all go on or all leave.
+  // Inside a job they all take the same steps, so that the barriers there cannot be left waiting.
+  bool dead = false;
+  const auto give_up = [&]() {
+    dead = true;
     *stop = 1;
     if (lane == 0) paged_err(kv, RTP_PAGED_ETIMEOUT);
   };
+  const auto consumers_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory"); };
   int st = 0;
   uint32_t phase = 0, jphase = 0, mphase = 0;
-  const auto all_meet = [&]() -> bool {
+  int verdict = 0;  // 2 per job, odd: leave
+  for (bool last = false; !last;) {
+    if (!mbar_wait(job_full, jphase)) give_up();
     __syncwarp();
     if (lane == 0) mbar_arrive(meet);
-    const bool ok = mbar_wait(meet, mphase);
+    if (!mbar_wait(meet, mphase)) give_up();
     mphase ^= 1u;
-    return ok;
-  };
-  for (bool last = false; !last;) {
-    if (!mbar_wait(job_full, jphase)) return gave_up();
+    int said = 0;
+    if (lane == 0) {
+      const int say = verdict + 2 + (dead || *stop ? 1 : 0);
+      said = atomicCAS(&sh.verdict, verdict, say);
+      if (said == verdict) said = say;
+    }
+    verdict = __shfl_sync(0xffffffffu, said, 0);
+    if (verdict & 1) return;
     jphase ^= 1u;
     const Job j = sh.job;
     last = j.last;
@@ -526,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
     if (a.logits) logit = a.logits + ((int64_t)j.row * d.Hq + j.g * d.group + j.h0) * a.cap;
 
     for (int i = 0; i < j.count; ++i) {
-      if (!mbar_wait(full + 8 * st, phase)) return gave_up();
+      if (!dead && !mbar_wait(full + 8 * st, phase)) give_up();
       const int base = sh.base[st][r0 / a.box] + (r0 & (a.box - 1));
-      if (base < j.len && (base + 16 > j.lo || base < j.sinks)) {
+      if (!dead && base < j.len && (base + 16 > j.lo || base < j.sinks)) {
         const uint32_t kb = ring + st * 2 * S::kHalf, vb = kb + S::kHalf;
         float z[NB][4] = {};
         if constexpr (!k8) {
@@ -678,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
           sh.l[warp][n * 8 + c2 + u] = x;
         }
       }
-    if (!all_meet()) return gave_up();
+    consumers_sync();
     constexpr int R = Sh::R;
     const int oh = tid / (R / 4), od = (tid % (R / 4)) * 4;  // this thread's head and dims in the exchange
     float f[NB][2];
@@ -709,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
           for (int e = 0; e < 4; ++e)
             sh.x[warp][n * 8 + c2 + (e & 1)][k * 16 + (k8 ? 2 * row + (e >> 1) : row + (e >> 1) * 8)] =
                 o[n][rd * (R / 16) + k][e] * f[n][e & 1];
-      if (!all_meet()) return gave_up();
+      consumers_sync();
       if (oh < j.nh) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -731,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnAr
           *(float4*)(a.part_o + (pslot * 16 + oh) * D + rd * R + od) = x;
         }
       }
-      if (!all_meet()) return gave_up();
+      consumers_sync();
     }
     if (od == 0 && oh < j.nh) {
       if (j.whole) {
@@ -764,6 +790,18 @@ __device__ void join_part(const AttnArgs& a, float bias, int c0, int hrow) {
   uint16_t* out = (uint16_t*)d.out + r * d.out_stride + (int64_t)h * D;
   const int64_t at = (int64_t)r * d.Hq + h;
   const auto part = [&](int i) { return (2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0)) * 16 + hrow; };
+  // the first parts' outputs, in flight while their weights are formed: a warp takes every
+  // kJoinWarps-th part
+  constexpr int V = D / 32, kAhead = 4;
+  const auto load = [&](int i, float* y) {
+    const float* p = a.part_o + part(i) * D + lane * V;
+    if constexpr (V == 4) *(float4*)y = *(const float4*)p;
+    else *(float2*)y = *(const float2*)p;
+  };
+  float first[kAhead][V];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (warp + u * kJoinWarps < n) load(warp + u * kJoinWarps, first[u]);
   // the parts' weights exp2(m - M), their sum of sums
   float m = -INFINITY;
   for (int i = tid; i < n; i += kJoinWarps * 32) {
@@ -790,26 +828,25 @@ __device__ void join_part(const AttnArgs& a, float bias, int c0, int hrow) {
   float L = 0.f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) L += red[1][w];
-  // the outputs: a warp takes every kJoinWarps-th part
-  constexpr int V = D / 32;
   float o[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) o[v] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += kJoinWarps) {
-    const float f = weight[i];
-    const float* p = a.part_o + part(i) * D + lane * V;
-    if constexpr (V == 4) {
-      const float4 x = *(const float4*)p;
-      o[0] = fmaf(x.x, f, o[0]);
-      o[1] = fmaf(x.y, f, o[1]);
-      o[2] = fmaf(x.z, f, o[2]);
-      o[3] = fmaf(x.w, f, o[3]);
-    } else {
-      const float2 x = *(const float2*)p;
-      o[0] = fmaf(x.x, f, o[0]);
-      o[1] = fmaf(x.y, f, o[1]);
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int i = warp + u * kJoinWarps;
+    if (i < n) {
+      const float f = weight[i];
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = fmaf(first[u][v], f, o[v]);
     }
+  }
+#pragma unroll 4
+  for (int i = warp + kAhead * kJoinWarps; i < n; i += kJoinWarps) {
+    float y[V];
+    load(i, y);
+    const float f = weight[i];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = fmaf(y[v], f, o[v]);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) so[warp][lane * V + v] = o[v];
