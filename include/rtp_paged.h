@@ -85,7 +85,8 @@ typedef struct {
  * q, k, v: DEVICE fp16 or bf16 (dtype; that of the pages unless those are e4m3), heads
  * contiguous, rows q_stride, k_stride, v_stride elements apart (multiples of 8).  q_out: rows
  * q_out_stride apart; it may be q itself.  q and q_out may both be NULL (n_q_heads is then
- * ignored).  max_new: an upper bound of the tokens of one sequence (sizes the launch). */
+ * ignored).  max_new: about the most tokens of one sequence (sizes a launch).  A page written to
+ * must belong to one sequence only. */
 rtp_status rtp_paged_append(const rtp_paged_kv* kv, const void* q, const void* k, const void* v, int32_t dtype,
                             int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_tokens,
                             int32_t n_q_heads, const int32_t* cu_new, int32_t max_new, const int32_t* seq_len,

@@ -181,7 +181,7 @@ __device__ __forceinline__ int token_seq(const int32_t* cu, int n_seqs, int t) {
 // Row groups of a token: ceil(Hq / R) of q, then ceil(Hkv / R) of k, then as many of v; `run` of them
 // per warp.  U groups are in flight at once.
 template <typename T, typename K, int D, int U>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a, int run, int runs, bool widen_bounds) {
+__global__ void __launch_bounds__(32 * kWarps, 5) append_kernel(const AppendArgs a, int run, int runs, bool widen_bounds) {
   constexpr int L = D / 16;       // lanes of a row
   constexpr int R = 32 / L;       // rows a warp holds at once
   constexpr int H = D / 2;
@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
                  (int64_t)h * D + c;
     x[0] = x[1] = make_uint4(0u, 0u, 0u, 0u);
     if (u < u1 && h < (is_q ? a.Hq : kv.Hkv)) {
-      x[0] = *(const uint4*)p;
-      x[1] = *(const uint4*)(p + H);
+      x[0] = __ldcs((const uint4*)p);
+      x[1] = __ldcs((const uint4*)(p + H));
     }
   };
   uint4 x[U][2];
@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs a,
       if (h >= (is_q ? a.Hq : kv.Hkv)) continue;
       if (is_q) {
         T* o = (T*)a.q_out + t * a.q_out_stride + (int64_t)h * D + c;
-        *(uint4*)o = Pack8<T>::of(z[0]);
-        *(uint4*)(o + H) = Pack8<T>::of(z[1]);
+        __stcs((uint4*)o, Pack8<T>::of(z[0]));
+        __stcs((uint4*)(o + H), Pack8<T>::of(z[1]));
       } else if (page >= 0) {
         K* o = (K*)(is_v ? kv.v + page * kv.vp + h * kv.vh + off * kv.vs : kv.k + page * kv.kp + h * kv.kh + off * kv.ks) + c;
         const float f = is_v ? kv.v_scale : kv.k_scale;
@@ -379,11 +379,14 @@ __global__ void __launch_bounds__(kBoundThreads) append_bounds_kernel(const Appe
   const int n = a.cu_new[b + 1] - a.cu_new[b];
   const int64_t cap = (int64_t)kv.max_pages << kv.page_shift;
   const int64_t s0 = a.seq_len[b], s1 = min(s0 + n, cap);
-  const int64_t i = (s0 >> kv.page_shift) + blockIdx.x;
-  const int64_t first = max(s0, i << kv.page_shift), last = min(s1, (i + 1) << kv.page_shift);
-  if (s0 < 0 || first >= last) return after_wait();
-  const int64_t base = i << kv.page_shift;
-  bounds_of<K, D>(kv, b, (int)i, blockIdx.y, (int)(first - base), (int)(last - base), true, sh);
+  if (s0 < 0 || s0 >= s1) return after_wait();
+  bool waited = false;
+  for (int64_t i = (s0 >> kv.page_shift) + blockIdx.x; i << kv.page_shift < s1; i += gridDim.x) {
+    const int64_t base = i << kv.page_shift, first = max(s0, base), last = min(s1, base + kv.page_size);
+    bounds_of<K, D>(kv, b, (int)i, blockIdx.y, (int)(first - base), (int)(last - base), true, sh);
+    waited = true;
+  }
+  if (!waited) after_wait();
 }
 
 template <typename K, int D>

@@ -564,8 +564,10 @@ cudaError_t run_select(const SelectPagesArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(page_score_kernel<T, K, D>, S::smem(kMaxM, kRowBlock), done);
   if (e != cudaSuccess) return e;
-  e = launch_after(page_score_kernel<T, K, D>, dim3((groups + rounds - 1) / rounds, a.kv.Hkv, blocks), 32 * kScoreWarps,
-                   S::smem(m_pad, row_block), st, a, row_block, m_pad, rounds, chunks);
+  // where every page is taken anyway no score is read
+  if (a.top < a.kv.max_pages)
+    e = launch_after(page_score_kernel<T, K, D>, dim3((groups + rounds - 1) / rounds, a.kv.Hkv, blocks), 32 * kScoreWarps,
+                     S::smem(m_pad, row_block), st, a, row_block, m_pad, rounds, chunks);
   if (e != cudaSuccess) return e;
   // Few lists: as many threads as a CTA has, for the latency; many: small CTAs, many at once.
   const int64_t lists = (int64_t)a.n_rows * a.kv.Hkv;

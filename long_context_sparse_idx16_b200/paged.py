@@ -39,8 +39,8 @@ class PagedKV(_paged.PagedKV):
         Append new tokens: norm and rotate q and k per head, write k and v to their pages.
         q: [T][Hq][D] or None; k, v: [T][Hkv][D] (rows may be slices of one projection's output).
         seq_lens: int32 [n_seqs], the lengths before the call.  cu_new: int32 [n_seqs + 1], the rows
-        of each sequence (None: one token for each); max_new bounds the tokens of one sequence
-        (default T).  positions: int32 [T] (default: each token's slot).  q_weight, k_weight: [D]
+        of each sequence (None: one token for each; rows behind the last are left alone); max_new:
+        about the most tokens of one sequence (default T, sizes a launch).  positions: int32 [T] (default: each token's slot).  q_weight, k_weight: [D]
         norm weights in the activations' dtype (None: no norm).  slot_positions: int32
         [n_seqs][Hkv][S], receives the position of each new slot.  Returns q_out ([T][Hq][D], which
         may be q itself), or None without q.  The caller advances its lengths.
