@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kT) page_pick_kernel(const SelectPagesArgs a, 
     s.low = ~0u;
     s.high = s.mag = s.q1 = 0u;
   }
+  if (chunks == 0) after_wait();  // no scoring kernel runs ahead of this one
   // the operator's inputs may be read ahead of the scores, its outputs be written
   int seq;
   const int len = paged_row(kv, a.row_seq, a.row_len, r, &seq);
@@ -569,10 +570,11 @@ cudaError_t run_select(const SelectPagesArgs& a, cudaStream_t st) {
     e = launch_after(page_score_kernel<T, K, D>, dim3((groups + rounds - 1) / rounds, a.kv.Hkv, blocks), 32 * kScoreWarps,
                      S::smem(m_pad, row_block), st, a, row_block, m_pad, rounds, chunks);
   if (e != cudaSuccess) return e;
+  const int scored = a.top < a.kv.max_pages ? chunks : 0;
   // Few lists: as many threads as a CTA has, for the latency; many: small CTAs, many at once.
   const int64_t lists = (int64_t)a.n_rows * a.kv.Hkv;
-  if (lists <= 2 * 148 || a.kv.max_pages > 8192) return run_pick<T, K, 1024>(a, chunks, st);
-  return run_pick<T, K, 128>(a, chunks, st);
+  if (lists <= 2 * 148 || a.kv.max_pages > 8192) return run_pick<T, K, 1024>(a, scored, st);
+  return run_pick<T, K, 128>(a, scored, st);
 }
 
 template <typename T, typename K>
