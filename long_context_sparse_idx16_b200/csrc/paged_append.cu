@@ -13,7 +13,12 @@
 // per warp, shared out over the lanes that need the same ones.  The runs are as long as still leaves
 // enough warps to fill the GPU (the host picks), since every warp forms the angles again.
 // One token per sequence: the K rows' warps also widen the page bounds.  In a chunk a page gets
-// several rows: a second kernel takes its bounds from the rows just written (in L2).
+// several rows: a second kernel takes its bounds from the rows just written (in L2: the other rows are
+// read and written as streams).
+//
+// Measured (one B200, 32 / 4 heads of 128, bf16, norms, bounds): 16384 tokens, 336 MB, in 69 us (4.9
+// TB/s), 60 us of it this kernel (5.6 TB/s of the 6.55 that a copy reaches); 64 tokens in 4 us.  Four
+// dims a lane instead of eight took 134 us (54.8 M warp instructions instead of 35.8 M).
 #include "paged.cuh"
 
 namespace rtp {
@@ -179,7 +184,8 @@ __device__ __forceinline__ int token_seq(const int32_t* cu, int n_seqs, int t) {
 }
 
 // Row groups of a token: ceil(Hq / R) of q, then ceil(Hkv / R) of k, then as many of v; `run` of them
-// per warp.  U groups are in flight at once.
+// per warp.  U groups are in flight at once: two where a warp has several (16384 tokens: 72 us, one
+// 85 us, four 82 us, for want of registers), one where it has one.
 template <typename T, typename K, int D, int U>
 __global__ void __launch_bounds__(32 * kWarps, 5) append_kernel(const AppendArgs a, int run, int runs, bool widen_bounds) {
   constexpr int L = D / 16;       // lanes of a row

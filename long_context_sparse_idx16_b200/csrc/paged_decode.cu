@@ -28,6 +28,11 @@
 //     contraction, and (transposed) two dims of two keys, which a byte permute splits over two
 //     output rows.  Their queries are scaled per head by a power of two into fp16's range, which is
 //     exact for values down to 2^-29 of the head's largest and off by 2^-40 of that below.
+// Measured (one B200, 32 / 4 heads of 128; a copy reaches 6.55 TB/s): 8 x 128K fp16 keys, 2.15 GB, in
+// 326 us (6.6 TB/s); 1M e4m3 keys, 1.07 GB, in 185 us (5.8 TB/s; the widening keeps the issue slots
+// half busy); 48 sequences of 1 to 32K keys, 363 MB, in 70 us (5.2 TB/s, of which 10 us are starts,
+// ends and the join); 777 keys in 9 us, latency.  Sixteen query rows to a tile (queries as the rows)
+// took 254 us at 1M e4m3 keys; unweighted problems took 132 us for the 48 sequences.
 // Accumulated weights need the final log-sum-exp: the scores go through the workspace in fp32 and
 // weights_kernel adds exp(s - lse) over the query heads, beside the join.
 #include <type_traits>
@@ -44,7 +49,8 @@ constexpr int kConsumers = 4;     // warps, 16 keys of a tile each
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kInline = 256;      // entries whose tile prefix every CTA forms by itself
 constexpr int kNoSlot = 0x7fff8000;  // beyond every length: a box none of whose slots is attended
-constexpr int kOverhead = 2;      // tiles' worth of time that a problem costs besides its tiles
+constexpr int kOverhead = 2;      // tiles' worth of time that a problem costs besides its tiles: about
+                                  // 1.5 us for the queries, the first look-up and the exchange of states
 constexpr int kMaxPerSm = 3;
 constexpr int kMaxSms = 160;      // what the workspace is sized for; a grid is at most kMaxPerSm times it
 

@@ -13,7 +13,12 @@
 //     infinities, NaN) all of them are scored exactly and a radix select over their 64-bit keys
 //     decides.
 // The bounds are read once per row (once per eight rows of a sequence that follow one another),
-// 4 D bytes a page in 16 bits: HBM bounds the scoring of decode rows, the tensor cores that of chunks.
+// 4 D bytes a page in 16 bits: HBM bounds the scoring of decode rows, the tensor cores and the issue
+// slots that of chunks.  Measured (one B200, 32 / 4 heads of 128): 8 rows of 2048 pages (33.5 MB) are
+// scored in 10 us and chosen from in 8 us; four lists of 16384 pages in 10 and 13 us; 1000 chunk rows
+// of 1022 pages (a third of the tensor pipe's rate) in 105 and 62 us.  All scores in fp64, a warp per
+// page, took 98 us, 94 us and 4.2 ms.  A cluster per list with the histogram in distributed shared
+// memory was slower than one CTA (59 against 47 us for the 2048-page case as a whole).
 #include "paged.cuh"
 #include "tc_umma.cuh"
 
