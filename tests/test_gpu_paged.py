@@ -657,3 +657,205 @@ def test_select_chunk_rows(group):
     for i, b in enumerate(seq):
         want = page_choice(c, f64(bounds), f64(x)[i], b, n[i], 0, 12, 1, 1)
         assert sel[i, 0].tolist() == want + [-1] * (12 - len(want)) and int(cnt[i, 0]) == len(want)
+
+
+# ---------------------------------------------------------------- layouts, offsets, many lists
+
+
+def padded(x, rows=1, dims=16):
+    """The same values in a larger allocation: pages, heads and slots with gaps between them."""
+    p, h, s, d = x.shape
+    big = torch.zeros((p, h + 1, s + rows, d + dims), dtype=x.dtype, device=x.device)
+    view = big[:, :h, :s, :d]
+    view.copy_(x)
+    return view
+
+
+@pytest.mark.parametrize("kv,q", [("fp16", "fp16"), ("e4m3", "bf16")])
+def test_padded_strides(kv, q):
+    """Strides that are no multiples of one another, different for K and V."""
+    c = Case([300, 0, 77], hq=8, hkv=2, d=64, page=32, kv=kv, q=q, seed=41, room=40, **SCALES.get(kv, {}))
+    c.k, c.v = padded(c.k), padded(c.v, 3, 32)
+    run_decode(c)
+    x = c.randn(3, 12, 64).to(c.qt).to(c.device)
+    cache = c.cache(bounds=torch.zeros((c.pool, 2, 2, 64), device=c.device).to(c.kt))
+    out = cache.append(x[:, :8], x[:, 8:10], x[:, 10:], c.ints(c.lens))
+    c.lens = [n + 1 for n in c.lens]
+    lens = c.ints(c.lens)
+    o, lse = cache.decode(out, lens, return_lse=True)
+    cache.check()
+    check_decode(c, out, o, lse, [(b, np.arange(n)) for b, n in enumerate(c.lens)])
+    cache.update_bounds(lens)
+    assert np.array_equal(f64(cache.bounds), stored_bounds(c))
+    run_evict(c, 64, 8, 2, 1)
+
+
+def test_pool_beyond_32_bits():
+    """Pages whose element offsets pass 2^31 (and byte offsets 2^32): append, bounds, decode, evict."""
+    free, _ = torch.cuda.mem_get_info()
+    pages, hkv, ps, d = 70000, 4, 64, 128
+    if free < 12 << 30:
+        pytest.skip("needs 12 GB")
+    c = Case([200, 130], hq=8, hkv=hkv, d=d, page=ps, kv="bf16", seed=42, room=80)
+    small_k, small_v, small_table = c.k, c.v, c.table.clone()
+    c.k, c.v = (torch.empty((pages, hkv, ps, d), dtype=c.kt, device=c.device) for _ in "kv")
+    far = torch.arange(pages - c.pool, pages)
+    c.k[far[0]:], c.v[far[0]:] = small_k, small_v
+    c.table = torch.where(small_table >= 0, small_table + (pages - c.pool), small_table).to(torch.int32)
+    bounds = torch.zeros((pages, hkv, 2, d), dtype=c.kt, device=c.device)
+    cache = c.cache(bounds=bounds)
+    x = c.randn(2, 16, d).to(c.qt).to(c.device)
+    q = cache.append(x[:, :8], x[:, 8:12], x[:, 12:], c.ints(c.lens))
+    lens = c.ints([201, 131])
+    cache.update_bounds(lens)
+    out, lse = cache.decode(q, lens, return_lse=True)
+    sel, cnt = cache.select_pages(q, lens, 2)
+    cache.check()
+    base = pages - c.pool  # back to a small copy for the fp64 side
+    c.k, c.v, c.table, c.lens = c.k[base:].clone(), c.v[base:].clone(), small_table, [201, 131]
+    check_decode(c, q, out, lse, [(b, np.arange(n)) for b, n in enumerate(c.lens)])
+    b64 = stored_bounds(c)
+    assert np.array_equal(f64(bounds[base:]), b64)
+    for r in range(2):
+        for g in range(hkv):
+            assert sel[r, g].tolist() == page_choice(c, b64, f64(q)[r], r, c.lens[r], g, 2, 0, 1)
+    # eviction moves rows between far pages
+    cap = cache.capacity
+    scores = torch.rand((2, hkv, cap), device=c.device)
+    pos = torch.arange(cap, device=c.device, dtype=torch.int32).expand(2, hkv, cap).contiguous()
+    s0 = scores.cpu().numpy()
+    cache.evict(lens, 100, scores, pos, n_recent=10)
+    after = f64(cache.k[base:])
+    before = f64(c.k)
+    for b, n in enumerate(c.lens):
+        for g in range(hkv):
+            _, src = evict_choice(s0[b, g], np.arange(cap), n, 100, 10, 0)
+            j = np.arange(100)
+            t = c.table[b].numpy()
+            assert np.array_equal(after[t[j // ps], g, j % ps], before[t[src // ps], g, src % ps])
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_many_page_lists(page):
+    """More lists than every CTA plans by itself, from empty to full, short and long pages."""
+    c = Case([page * 20 - 3, page * 7], hq=6, hkv=3, d=64, page=page, kv="fp16", seed=page)
+    r = np.random.default_rng(page)
+    rows = 130
+    seq = r.integers(0, 2, rows)
+    n = np.array([int(r.integers(0, c.lens[b] + 1)) for b in seq])
+    sel = np.full((rows, 3, 9), -1, dtype=np.int32)
+    cnt = r.integers(0, 10, (rows, 3)).astype(np.int32)
+    want = []
+    for i in range(rows):
+        per = []
+        for g in range(3):
+            pages = r.permutation(20)[:cnt[i, g]]
+            sel[i, g, :cnt[i, g]] = pages
+            per.append(np.array([j for p in pages for j in range(p * page, p * page + page) if j < n[i]], dtype=int))
+        want.append((int(seq[i]), per))
+    q = c.randn(rows, 6, 64).to(c.qt).to(c.device)
+    cache = c.cache()
+    out, lse = cache.decode(q, c.ints(n.tolist()), row_seq=c.ints(seq.tolist()), return_lse=True,
+                            pages=(torch.from_numpy(sel).to(c.device), torch.from_numpy(cnt).to(c.device)))
+    cache.check()
+    check_decode(c, q, out, lse, want)
+
+
+def test_decode_writes_over_its_queries():
+    c = Case([700, 64, 0, 2100], hq=16, hkv=2, d=128, page=64, kv="bf16", seed=51)
+    q = c.randn(4, 16, 128).to(c.qt).to(c.device)
+    cache = c.cache()
+    want = cache.decode(q, c.ints(c.lens))
+    got = q.clone()
+    assert cache.decode(got, c.ints(c.lens), out=got) is got
+    assert torch.equal(got, want)
+
+
+def test_wider_slot_arrays_and_captured_eviction():
+    """Scores and positions with more slots than the table; append of a chunk, eviction and the bounds
+    behind it captured and replayed with other contents."""
+    c = Case([150, 90, 33], hq=4, hkv=2, d=64, page=16, kv="fp16", seed=61, room=50)
+    bounds = torch.zeros((c.pool, 2, 2, 64), dtype=c.kt, device=c.device)
+    cache = c.cache(bounds=bounds)
+    S = cache.capacity + 37
+    scores = torch.zeros((3, 2, S), device=c.device)
+    pos = torch.full((3, 2, S), -1, dtype=torch.int32, device=c.device)
+    lens = c.ints(c.lens)
+    cu = c.ints([0, 40, 41, 60])
+    x = c.randn(64, 8, 64).to(c.qt).to(c.device)
+    out = torch.zeros((64, 4, 64), dtype=c.qt, device=c.device)
+
+    def step():
+        cache.append(x[:, :4], x[:, 4:6], x[:, 6:], lens, cu_new=cu, max_new=1, q_out=out, slot_positions=pos)
+        n = lens + (cu[1:] - cu[:-1])
+        cache.decode(out[:3], n, scores=scores)
+        return cache.evict(n, 64, scores, pos, n_recent=8, n_sink=2)
+
+    k0, v0 = c.k.clone(), c.v.clone()
+
+    def reset(seed):
+        g = torch.Generator().manual_seed(seed)
+        c.k.copy_(k0)
+        c.v.copy_(v0)
+        bounds.zero_()
+        out.zero_()
+        x.copy_(torch.randn(x.shape, generator=g).to(c.qt))
+        scores.copy_(torch.rand(scores.shape, generator=g))
+        pos.copy_(torch.arange(S, dtype=torch.int32).expand(3, 2, S))
+        for b, n in enumerate(c.lens):
+            scores[b, :, n:] = 0.0
+            pos[b, :, n:] = -1
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        reset(1)
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    reset(2)
+    with torch.cuda.graph(graph):
+        new, _, _ = step()
+    for seed in (3, 4):
+        reset(seed)
+        graph.replay()
+        got = [t.clone() for t in (c.k, c.v, bounds, scores, pos, out, new)]
+        reset(seed)
+        n2, _, _ = step()
+        want = [c.k, c.v, bounds, scores, pos, out, n2]
+        # unused slots hold NaN
+        assert all(torch.equal(a.nan_to_num(7.0) if a.is_floating_point() else a, b.nan_to_num(7.0) if b.is_floating_point() else b)
+                   for a, b in zip(got, want))
+        assert new.tolist() == [64, 64, 52]
+        assert bool((out[60:] == 0).all())  # rows behind the last sequence
+        assert bool((pos[:, :, 64:] == -1).all()) and bool((scores[:, :, 64:] == 0).all())
+    cache.check()
+
+
+def test_two_graphs_at_once():
+    """Two captured steps on two streams, replayed together, keep their own workspaces."""
+    c = Case([4000, 900, 17], hq=8, hkv=2, d=128, page=64, kv="fp16", seed=71)
+    bounds = torch.from_numpy(stored_bounds(c)).float().to(c.kt).to(c.device)
+    cache = c.cache(bounds=bounds)
+    lens = c.ints(c.lens)
+    qs = [c.randn(3, 8, 128).to(c.qt).to(c.device) for _ in range(2)]
+
+    def step(q):
+        pages = cache.select_pages(q, lens, 9, n_first=1)
+        return cache.decode(q, lens), cache.decode(q, lens, pages=pages), pages[0]
+
+    want = [[t.clone() for t in step(q)] for q in qs]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for q, st in zip(qs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            outs.append(step(q))
+        graphs.append(g)
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for w, o in zip(want, outs):
+            assert all(torch.equal(a, b) for a, b in zip(w, o))
