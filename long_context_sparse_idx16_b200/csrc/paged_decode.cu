@@ -51,13 +51,14 @@ constexpr int kInline = 256;      // entries whose tile prefix every CTA forms b
 constexpr int kNoSlot = 0x7fff8000;  // beyond every length: a box none of whose slots is attended
 constexpr int kOverhead = 2;      // tiles' worth of time that a problem costs besides its tiles: about
                                   // 1.5 us for the queries, the first look-up and the exchange of states
-constexpr int kMaxPerSm = 3;
+constexpr int kMaxPerSm = 4;
 constexpr int kMaxSms = 160;      // what the workspace is sized for; a grid is at most kMaxPerSm times it
 
 // Eight query heads need half the registers of sixteen: three CTAs per SM instead of two, with
-// rings of 64 KB instead of 96 KB.
-constexpr int per_sm(int octets) { return octets == 1 ? 3 : 2; }
-constexpr int ring_bytes(int octets) { return octets == 1 ? 64 * 1024 : 96 * 1024; }
+// rings of 64 KB instead of 96 KB.  Four with rows of 64 values, whose stages are small and whose tiles
+// cost more in steps than in bytes: 8 x 128K keys of 64 values 176 -> 165 us (e4m3 126 -> 114 us).
+constexpr int per_sm(int octets, int D) { return octets == 1 ? (D == 64 ? 4 : 3) : 2; }
+constexpr int ring_bytes(int octets, int D) { return octets == 1 ? (D == 64 ? 40 : 64) * 1024 : 96 * 1024; }
 
 struct AttnArgs {
   DecodeArgs d;
@@ -159,7 +160,7 @@ struct Stage {
   static constexpr int kBlocks = kBytes / kRow;
   static constexpr int kHalf = kTile * kBytes;                // K, and V
   static constexpr int stages(int octets) {
-    return ring_bytes(octets) / (2 * kHalf) > 8 ? 8 : ring_bytes(octets) / (2 * kHalf);
+    return ring_bytes(octets, D) / (2 * kHalf) > 8 ? 8 : ring_bytes(octets, D) / (2 * kHalf);
   }
   // byte offset of 16-byte chunk ch of row r
   static __device__ __forceinline__ uint32_t at(int r, int ch) {
@@ -303,7 +304,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 template <typename QT, typename K, int D, int NB>
-__global__ void __launch_bounds__(kThreads, per_sm(NB)) attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap km,
+__global__ void __launch_bounds__(kThreads, per_sm(NB, D)) attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap km,
                                                                     const __grid_constant__ CUtensorMap vm) {
   using S = Stage<K, D>;
   using Sh = Shared<NB, D>;
@@ -987,13 +988,13 @@ template <typename QT, typename K, int D, int NB>
 cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   using S = Stage<K, D>;
   constexpr size_t smem = (size_t)S::stages(NB) * 2 * S::kHalf + sizeof(Shared<NB, D>);
-  static_assert((smem + 1024) * per_sm(NB) <= 228 * 1024, "the CTAs of an SM share 228 KB");
+  static_assert((smem + 1024) * per_sm(NB, D) <= 228 * 1024, "the CTAs of an SM share 228 KB");
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(attn_kernel<QT, K, D, NB>, smem, done);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)a.n_entries * a.mult * (a.whole ? 1 : slots_of(a) / kTile + 1 + kOverhead);
   const int sms = device_sms();
-  int64_t grid = (int64_t)per_sm(NB) * (sms < kMaxSms ? sms : kMaxSms);
+  int64_t grid = (int64_t)per_sm(NB, D) * (sms < kMaxSms ? sms : kMaxSms);
   if (grid > most) grid = most;
   if (a.n_entries > kInline && (e = launch_after(plan_kernel, dim3(1), 1024, 0, st, a)) != cudaSuccess) return e;
   e = launch_after(attn_kernel<QT, K, D, NB>, dim3((unsigned)grid), kThreads, smem, st, a, km, vm);
