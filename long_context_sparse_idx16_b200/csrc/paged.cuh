@@ -79,20 +79,6 @@ __device__ __forceinline__ int64_t paged_page(const PagedView& p, int b, int i) 
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__nv_fp8_e4m3 x) { return (float)x; }
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float x) {
-  return __float2half_rn(x);
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ __nv_fp8_e4m3 from_f32<__nv_fp8_e4m3>(float x) {
-  return __nv_fp8_e4m3(x);  // nearest, saturating at 448, NaN kept
-}
 
 // ---- products on the tensor cores, fp16 or bf16 operands
 

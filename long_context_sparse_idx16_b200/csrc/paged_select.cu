@@ -546,10 +546,12 @@ cudaError_t run_pick(const SelectPagesArgs& a, int chunks, cudaStream_t st) {
                        (size_t)a.group * (kExactPages * sizeof(unsigned long long) + a.kv.D * sizeof(T));
   constexpr size_t kMost = kExactPages * 2 * kD * sizeof(T) + 64 * (kExactPages * 8 + kD * sizeof(T));  // of `fixed`
   cudaError_t e;
-  if (a.kv.max_pages > kPagesInSmem) {
-    static std::atomic<uint64_t> done{0};
-    if ((e = allow_smem(page_pick_kernel<T, K, kT, false>, kMost, done)) != cudaSuccess) return e;
-    return launch_after(page_pick_kernel<T, K, kT, false>, grid, kT, fixed, st, a, chunks);
+  if constexpr (kT == 1024) {  // (the small CTAs take short lists only)
+    if (a.kv.max_pages > kPagesInSmem) {
+      static std::atomic<uint64_t> done{0};
+      if ((e = allow_smem(page_pick_kernel<T, K, kT, false>, kMost, done)) != cudaSuccess) return e;
+      return launch_after(page_pick_kernel<T, K, kT, false>, grid, kT, fixed, st, a, chunks);
+    }
   }
   static std::atomic<uint64_t> done{0};
   if ((e = allow_smem(page_pick_kernel<T, K, kT, true>, kMost + kPagesInSmem * sizeof(float), done)) != cudaSuccess) return e;

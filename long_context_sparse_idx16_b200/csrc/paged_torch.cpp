@@ -4,6 +4,8 @@
 // because a decode step's kernels take a few microseconds: checking five tensors and passing two
 // dozen arguments through ctypes took 20 us a call, this takes 2.
 #include <ATen/cuda/CUDAContext.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/extension.h>
 
@@ -124,7 +126,7 @@ class PagedKV {
     if (q) {
       qs = heads(*q, "q", T, -1, &dt);
       hq = q->size(1);
-      if (!q_out) q_out = at::empty({T, hq, h_.head_dim}, q->options());
+      if (!q_out) q_out = make({T, hq, h_.head_dim}, dt);
       os = heads(*q_out, "q_out", T, hq, &dt);
     }
     if (T)
@@ -163,17 +165,17 @@ class PagedKV {
     if (scores) st = slots(*scores, "scores", at::kFloat);
     const at::ScalarType dt = q.scalar_type();
     const Guard guard(*this, stream);
-    if (!out) out = at::empty({n, hq, h_.head_dim}, q.options());
+    if (!out) out = make({n, hq, h_.head_dim}, dt);
     const int64_t os = heads(*out, "out", n, hq, &dt);
     OptTensor lse;
-    if (return_lse) lse = at::empty({n, hq}, q.options().dtype(at::kFloat));
+    if (return_lse) lse = make({n, hq}, at::kFloat);
     if (n) {
       const size_t need = rtp_paged_decode_workspace(&h_, num(n), num(hq), scores ? 1 : 0);
-      const Tensor ws = workspace(need);
+      const at::DataPtr ws = workspace(need);
       check(rtp_paged_decode(&h_, q.data_ptr(), code_of(dt), qs, num(n), num(hq), static_cast<int32_t*>(ptr(row_seq)),
                              seq_lens.data_ptr<int32_t>(), num(window), num(n_sink), (float)sm_scale, sel, cnt, ss,
                              out->data_ptr(), os, static_cast<float*>(ptr(lse)), static_cast<float*>(ptr(scores)), st,
-                             ws.data_ptr(), need, guard.stream));
+                             ws.get(), need, guard.stream));
     }
     if (return_lse) return py::make_tuple(*out, *lse);
     return py::cast(*out);
@@ -186,15 +188,15 @@ class PagedKV {
     if (!bounds_) bad("the cache keeps no page bounds");
     if (top_pages < 1) bad("top_pages must be at least 1");
     const Guard guard(*this, stream);
-    const Tensor sel = at::empty({n, h_.n_kv_heads, top_pages}, seq_lens.options());
-    const Tensor cnt = at::empty({n, h_.n_kv_heads}, seq_lens.options());
+    const Tensor sel = make({n, h_.n_kv_heads, top_pages}, at::kInt);
+    const Tensor cnt = make({n, h_.n_kv_heads}, at::kInt);
     if (n) {
       const size_t need = rtp_paged_select_workspace(&h_, num(n), num(hq));
-      const Tensor ws = workspace(need);
+      const at::DataPtr ws = workspace(need);
       check(rtp_paged_select(&h_, q.data_ptr(), code_of(q.scalar_type()), qs, num(n), num(hq),
                              static_cast<int32_t*>(ptr(row_seq)), seq_lens.data_ptr<int32_t>(), num(top_pages),
                              num(n_first), num(n_recent), sel.data_ptr<int32_t>(), top_pages, cnt.data_ptr<int32_t>(),
-                             ws.data_ptr(), need, guard.stream));
+                             ws.get(), need, guard.stream));
     }
     return py::make_tuple(sel, cnt);
   }
@@ -209,12 +211,12 @@ class PagedKV {
                                       std::tuple{&po, "out_positions", at::kInt}})
       if (slots(*t, name, dt) != st) bad(name, ": expected ", std::to_string(st), " slots, as scores have");
     const Guard guard(*this, stream);
-    const Tensor len = at::empty({h_.n_seqs}, seq_lens.options());
+    const Tensor len = make({h_.n_seqs}, at::kInt);
     const size_t need = rtp_paged_evict_workspace(&h_, st);
-    const Tensor ws = workspace(need);
+    const at::DataPtr ws = workspace(need);
     check(rtp_paged_evict(&h_, seq_lens.data_ptr<int32_t>(), num(budget), num(n_recent), num(n_sink),
                           scores.data_ptr<float>(), positions.data_ptr<int32_t>(), st, so.data_ptr<float>(),
-                          po.data_ptr<int32_t>(), len.data_ptr<int32_t>(), ws.data_ptr(), need, guard.stream));
+                          po.data_ptr<int32_t>(), len.data_ptr<int32_t>(), ws.get(), need, guard.stream));
     if (bounds_) check(rtp_paged_bounds(&h_, len.data_ptr<int32_t>(), guard.stream));
     return py::make_tuple(len, so, po);
   }
@@ -250,8 +252,14 @@ class PagedKV {
     return (int32_t)x;
   }
 
-  Tensor workspace(size_t n) const {
-    return at::empty({(int64_t)std::max<size_t>(n, 16)}, table_.options().dtype(at::kByte));
+  // A new tensor, and a workspace that lives until the call returns (its memory is then torch's to give
+  // to later work of the same stream).  Both straight from torch's allocator: through the dispatcher an
+  // allocation takes 0.5 us more, and a decode call makes three.
+  Tensor make(at::IntArrayRef shape, at::ScalarType dt) const {
+    return at::detail::empty_cuda(shape, dt, device_, std::nullopt);
+  }
+  static at::DataPtr workspace(size_t n) {
+    return c10::cuda::CUDACachingAllocator::get()->allocate(std::max<size_t>(n, 16));
   }
 
   void is(const Tensor& t, const char* name, at::ScalarType dt) const {
