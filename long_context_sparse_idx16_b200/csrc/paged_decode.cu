@@ -7,7 +7,7 @@
 // heads per KV head, at most 16 in one pass), so HBM bounds it; the split follows from that:
 //   * The keys of all problems (row, KV head, block of 8 or 16 query heads) are cut into tiles of 64
 //     and numbered through, each problem counting kOverhead tiles more than it has (what starting
-//     and ending it costs).  CTA c of a grid of two or three per SM takes the numbers [c T / G, (c + 1)
+//     and ending it costs).  CTA c of a grid of two to four per SM takes the numbers [c T / G, (c + 1)
 //     T / G), so every SM has the same work whatever the lengths are, and the host need not know
 //     them.  A problem that crosses CTAs leaves partial results (running max, sum, unnormalised
 //     output), at most two per CTA, which join_kernel adds up in CTA order.
