@@ -644,13 +644,16 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB, D)) attn_kernel(const Att
               for (int e = 0; e < 4; ++e) o[n][k][e] *= f[e & 1];
           }
         }
-        uint32_t p[NB][2];  // weights as the B operand: keys (contraction) by heads
+        // Weights as the B operand: keys (contraction) by heads.  The difference to the maximum comes
+        // first: it is 0 for the largest score, whatever its size, so no weight passes 2^kBias and the sums
+        // carry exactly this factor.  (m - kBias would be rounded from 2^24 on, up to a weight of 2^16.)
+        uint32_t p[NB][2];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            w[e] = fast_exp2(z[n][e] - ((m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1]) - kBias));
+            w[e] = fast_exp2((z[n][e] - (m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1])) + kBias);
           l[n][0] += w[0] + w[2];
           l[n][1] += w[1] + w[3];
           p[n][0] = movmatrix(pack2<MT>(w[0], w[1]));

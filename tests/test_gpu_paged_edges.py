@@ -1,0 +1,68 @@
+"""Paged-cache operators on the GPU at the edges of what their arguments allow, against the
+definitions in fp64 (tests/paged_ref.py)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from paged_ref import TINY, U, Case, check_decode, f64
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [("fp16", "fp16"), ("bf16", "bf16"), ("e4m3", "fp16"), ("e4m3", "bf16")]
+
+
+# ---------------------------------------------------------------- scores far from zero
+
+
+def far_scores(kv, q, z, other, n, where, seed):
+    """One sequence of n keys and one KV head of two query heads whose base-2 scores are known to the
+    last bit: `z` at the slots `where[0]`, `other` at where[1], far below both everywhere else.  Every
+    product and sum behind them is a small multiple of a power of two, exact in fp32 (terms further than
+    2^-22 from one another do not meet).  Values are random.  Returns the case, the queries and sm_scale."""
+    c = Case([n], hq=2, hkv=1, d=64, page=64, kv=kv, q=q, seed=seed, k_scale=2.0**6 if kv == "e4m3" else 1.0)
+    # scores: q0 k0 + 2 k1, times k_scale.  e4m3 keys are at most 448, and multiples of 2^-9
+    q0 = 2.0**13 if abs(z) > 2**20 else 8.0
+    queries = torch.zeros(1, 2, 64)
+    queries[..., 0], queries[..., 1] = q0, 2.0
+    top = math.copysign(2.0 ** math.floor(math.log2(abs(z))), z)  # the part of the score that dim 0 makes
+    k = torch.zeros(n, 64)
+    k[:, 0], k[:, 1] = top / q0 / c.k_scale, -192.0  # far below the others in base 2
+    for slots, s in zip(where, (z, other)):
+        k[slots, 1] = (s - top) / 2.0 / c.k_scale
+    assert torch.equal(k.to(c.kt).float(), k)
+    pages = torch.zeros(c.pool, 1, 64, 64)
+    for i in range(-(-n // 64)):
+        rows = k[i * 64:(i + 1) * 64]
+        pages[int(c.table[0, i]), 0, :len(rows)] = rows
+    c.k = c.put(pages)
+    # sm_scale * log2(e) = 1 to fp32's last bit
+    sm = float(np.float32(math.log(2.0)))
+    assert np.float32(sm * float(np.float32(c.k_scale)) * 1.4426950408889634) == np.float32(c.k_scale)
+    return c, queries.to(c.qt).to(c.device), sm
+
+
+FAR = [(2**24 + 20, 2**24 + 16), (2**25 + 8, 2**25), (2**26 + 16, 2**26 + 16), (2**27 + 32, 2**27 + 32),
+       (-(2**24) - 4, -(2**24) - 8), (-(2**25) - 8, -(2**25) - 16), (-(2**27) - 32, -(2**27) - 32), (100, 96)]
+
+
+@pytest.mark.parametrize("kv,q", TYPES)
+@pytest.mark.parametrize("z,other", FAR)
+@pytest.mark.parametrize("n", [200, 20000])
+def test_decode_of_far_scores(kv, q, z, other, n):
+    """Finite scores, however large, give the weights that their differences say: here 1 and
+    2^(other - z), exactly, so that only the exponential (2^-21 with the sums) and the output round."""
+    where = [[7], [n - 3]]
+    c, x, sm = far_scores(kv, q, z, other, n, where, 1)
+    out, lse = c.cache().decode(x, c.ints([n]), sm_scale=sm, return_lse=True)
+    _, v = c.rows64(0, 0, np.arange(n))
+    p = np.zeros(n)
+    p[where[0]], p[where[1]] = 1.0, 2.0 ** (other - z)
+    want = p @ v / p.sum()
+    # (weights below 2^-24 of the largest are 0 in bf16 as in exact sums rounded to the output)
+    tol = U[c.qt] * np.abs(want) * 1.01 + 2.0**-20 * (p @ np.abs(v)) + TINY[c.qt]
+    for h in range(2):
+        assert np.all(np.abs(f64(out)[0, h] - want) <= tol), (h, f64(out)[0, h, :4], want[:4])
+        natural = (z + math.log2(p.sum())) * math.log(2.0)
+        assert abs(float(lse[0, h]) - natural) <= 2.0**-22 * abs(natural) + 2.0**-20
