@@ -33,8 +33,8 @@
 // half busy); 48 sequences of 1 to 32K keys, 363 MB, in 70 us (5.2 TB/s, of which 10 us are starts,
 // ends and the join); 777 keys in 9 us, latency.  Sixteen query rows to a tile (queries as the rows)
 // took 254 us at 1M e4m3 keys; unweighted problems took 132 us for the 48 sequences.
-// Accumulated weights need the final log-sum-exp: the scores go through the workspace in fp32 and
-// weights_kernel adds exp(s - lse) over the query heads, beside the join.
+// Accumulated weights need the final sums: the scores go through the workspace in fp32 and
+// weights_kernel adds exp2((s - M) - log2 L) over the query heads, beside the join.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -68,7 +68,7 @@ struct AttnArgs {
   int whole;             // problems are never split (short caches)
   int n_entries, mult;   // dense: rows, Hkv * blocks; page lists: rows * Hkv, blocks
   int64_t* prefix;       // [n_entries + 1] tiles (with overhead) of the entries before, one problem each
-  float* lse2;           // [rows][Hq] base-2 log-sum-exp, or NULL
+  float2* sums;          // [rows][Hq] largest base-2 score and log2 of the sum of weights beside it, or NULL
   float* logits;         // [rows][Hq][cap] base-2 scores, or NULL
   int64_t cap;
   int4* split;           // [CTAs] problem that the CTA begins and others go on with: (row, query head,
@@ -109,6 +109,16 @@ __device__ __forceinline__ Entry entry_of(const AttnArgs& a, int e) {
   }
   n.tiles = (n.len + kTile - 1) / kTile - n.t_skip;
   return n;
+}
+
+// From the largest base-2 score M and the sum L of 2^(score - M + bias): the natural log-sum-exp; and M
+// with log2 of the sum beside it, which a weight is formed from.  The two stay apart there: their sum
+// would lose the logarithm where M is large.
+__device__ __forceinline__ float lse_of(float M, float L, float bias) {
+  return (L == 0.f ? -INFINITY : M + (log2f(L) - bias)) * 0.6931471805599453f;
+}
+__device__ __forceinline__ float2 sums_of(float M, float L, float bias) {
+  return L == 0.f ? make_float2(0.f, INFINITY) : make_float2(M, log2f(L) - bias);
 }
 
 // Length of an entry's problem in the numbering: its tiles and the overhead (1 if it is not to be split).
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB, D)) attn_kernel(const Att
     for (int x = tid; x < nh * D / 8; x += kThreads) ((uint4*)out)[x] = make_uint4(0u, 0u, 0u, 0u);
     for (int x = tid; x < nh; x += kThreads) {
       if (d.lse) d.lse[(int64_t)r * d.Hq + h + x] = -INFINITY;
-      if (a.lse2) a.lse2[(int64_t)r * d.Hq + h + x] = -INFINITY;
+      if (a.sums) a.sums[(int64_t)r * d.Hq + h + x] = make_float2(0.f, INFINITY);
     }
   }
   if ((int)blockIdx.x >= ranges.ctas) return;
@@ -771,10 +781,9 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB, D)) attn_kernel(const Att
     }
     if (od == 0 && oh < j.nh) {
       if (j.whole) {
-        const float y = L == 0.f ? -INFINITY : M + (log2f(L) - kBias);
         const int64_t at = (int64_t)j.row * d.Hq + j.g * d.group + j.h0 + oh;
-        if (d.lse) d.lse[at] = y * 0.6931471805599453f;
-        if (a.lse2) a.lse2[at] = y;
+        if (d.lse) d.lse[at] = lse_of(M, L, kBias);
+        if (a.sums) a.sums[at] = sums_of(M, L, kBias);
       } else {
         a.part_ml[pslot * 16 + oh] = make_float2(M, L);
       }
@@ -872,28 +881,25 @@ __device__ void join_part(const AttnArgs& a, float bias, int c0, int hrow) {
     const float inv = kv.v_scale / L;
     *(uint32_t*)(out + x) = L == 0.f ? 0u : pack2<QT>(y0 * inv, y1 * inv);
   }
-  if (tid == 0) {
-    const float y = L == 0.f ? -INFINITY : M + (log2f(L) - bias);
-    if (d.lse) d.lse[at] = y * 0.6931471805599453f;
-  }
+  if (tid == 0 && d.lse) d.lse[at] = lse_of(M, L, bias);
 }
 
-// scores[row][g][j] += sum over g's heads of exp2(logit - lse2), for the slots attended.  The
-// log-sum-exp of a split problem is joined here again, a warp per head.
+// scores[row][g][j] += sum over g's heads of exp2((logit - M) - log2 L), for the slots attended.  M and
+// log2 L of a split problem are joined here again, a warp per head.
 __device__ void add_weights(const AttnArgs& a, float bias, int chunk, int chunks) {
   const DecodeArgs& d = a.d;
   const PagedView& kv = d.kv;
   const int g = blockIdx.y, r = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float lse[64];
+  __shared__ float2 sums[64];
   const Entry n = entry_of(a, r);
   const int slots = n.sinks + n.len - n.lo;
   if (chunk * (kJoinWarps * 32) >= slots) return;
   const int heads = 8 * a.octets;
   for (int u = warp; u < d.group; u += kJoinWarps) {
     const int2 c = a.span[(int64_t)r * a.mult + g * a.blocks + u / heads];
-    float y;
+    float2 y;
     if (c.x < 0) {
-      y = a.lse2[(int64_t)r * d.Hq + g * d.group + u];
+      y = a.sums[(int64_t)r * d.Hq + g * d.group + u];
     } else {
       float m = -INFINITY, l = 0.f;
       for (int i = c.x + lane; i <= c.y; i += 32) {
@@ -904,9 +910,9 @@ __device__ void add_weights(const AttnArgs& a, float bias, int chunk, int chunks
       }
       const float M = warp_max(m);
       const float L = warp_sum(l * exp2f(m - (M == -INFINITY ? 0.f : M)));
-      y = L == 0.f ? -INFINITY : M + (log2f(L) - bias);
+      y = sums_of(M, L, bias);
     }
-    if (lane == 0) lse[u] = y == -INFINITY ? INFINITY : y;
+    if (lane == 0) sums[u] = y;
   }
   __syncthreads();
   const float* lg = a.logits + ((int64_t)r * d.Hq + g * d.group) * a.cap;
@@ -916,7 +922,7 @@ __device__ void add_weights(const AttnArgs& a, float bias, int chunk, int chunks
     if (paged_page(kv, n.seq, j >> kv.page_shift) < 0) continue;
     float w = 0.f;
 #pragma unroll 8
-    for (int u = 0; u < d.group; ++u) w += fast_exp2(lg[u * a.cap + j] - lse[u]);
+    for (int u = 0; u < d.group; ++u) w += fast_exp2((lg[u * a.cap + j] - sums[u].x) - sums[u].y);
     sc[j] += w;
   }
 }
@@ -951,7 +957,7 @@ int device_sms() {
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Layout {
-  size_t prefix, split, span, lse2, ml, o, logits, total;
+  size_t prefix, split, span, sums, ml, o, logits, total;
 };
 Layout layout_of(const rtp_paged_kv* kv, int n_rows, int n_q_heads, bool scores) {
   Layout l;
@@ -968,7 +974,7 @@ Layout layout_of(const rtp_paged_kv* kv, int n_rows, int n_q_heads, bool scores)
   l.o = take(parts * kv->head_dim * sizeof(float));
   const int group = n_q_heads / kv->n_kv_heads, blocks = group <= 8 ? 1 : (group + 15) / 16;
   l.span = take(scores ? (size_t)n_rows * kv->n_kv_heads * blocks * sizeof(int2) : 0);
-  l.lse2 = take(scores ? (size_t)n_rows * n_q_heads * sizeof(float) : 0);
+  l.sums = take(scores ? (size_t)n_rows * n_q_heads * sizeof(float2) : 0);
   l.logits = take(scores ? (size_t)n_rows * n_q_heads * kv->max_pages * kv->page_size * sizeof(float) : 0);
   l.total = at;
   return l;
@@ -1044,7 +1050,7 @@ cudaError_t launch_paged_decode(const DecodeArgs& d, const rtp_paged_kv* kv, int
   a.part_o = reinterpret_cast<float*>(ws + l.o);
   if (d.scores) {
     a.span = reinterpret_cast<int2*>(ws + l.span);
-    a.lse2 = reinterpret_cast<float*>(ws + l.lse2);
+    a.sums = reinterpret_cast<float2*>(ws + l.sums);
     a.logits = reinterpret_cast<float*>(ws + l.logits);
   }
   CUtensorMap km, vm;

@@ -66,3 +66,22 @@ def test_decode_of_far_scores(kv, q, z, other, n):
         assert np.all(np.abs(f64(out)[0, h] - want) <= tol), (h, f64(out)[0, h, :4], want[:4])
         natural = (z + math.log2(p.sum())) * math.log(2.0)
         assert abs(float(lse[0, h]) - natural) <= 2.0**-22 * abs(natural) + 2.0**-20
+
+
+@pytest.mark.parametrize("kv,q", TYPES)
+@pytest.mark.parametrize("z,other", FAR)
+@pytest.mark.parametrize("n", [200, 20000])
+def test_accumulated_weights_of_far_scores(kv, q, z, other, n):
+    """The weights added up are those of the softmax: they sum to the number of query heads, at scores
+    beside which the logarithm of their sum is below fp32's last bit."""
+    where = [[7, 100], [n - 3]]
+    c, x, sm = far_scores(kv, q, z, other, n, where, 2)
+    kvc = c.cache()
+    scores = torch.zeros((1, 1, kvc.capacity), device=c.device)
+    kvc.decode(x, c.ints([n]), sm_scale=sm, scores=scores)
+    p = np.zeros(kvc.capacity)
+    p[where[0]], p[where[1]] = 1.0, 2.0 ** (other - z)
+    want = 2 * p / p.sum()
+    # the exponential, the logarithm of the sum (at most 2) and the sum of two heads; the exponent's rounding
+    tol = (2.0**-20 + 2.0**-24 * (z - other + 2)) * want
+    assert np.all(np.abs(f64(scores)[0, 0] - want) <= tol), (f64(scores)[0, 0][[7, 100, n - 3]], want[[7, 100, n - 3]])
