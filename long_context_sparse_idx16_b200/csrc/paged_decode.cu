@@ -538,8 +538,9 @@ __global__ void __launch_bounds__(kThreads, per_sm(NB, D)) attn_kernel(const Att
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int ex = (int)(__float_as_uint(top) >> 23);  // biased exponent
-        // 2^(14 - e) and its inverse, both normal numbers; 1 for zeros, infinities and the like
-        const bool odd = ex < 15 || ex > 253;
+        // 2^(14 - e) and its inverse, both normal numbers: 2^126 at most, which brings bf16's least values
+        // (2^-133) to 2^-7; 1 for infinities
+        const bool odd = ex > 254;
         const float up = odd ? 1.f : __uint_as_float((uint32_t)min(254 + 14 - ex, 253) << 23);
         const float down = odd ? 1.f : __uint_as_float((uint32_t)max(ex - 14, 1) << 23);
 #pragma unroll

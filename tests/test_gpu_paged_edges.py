@@ -85,3 +85,23 @@ def test_accumulated_weights_of_far_scores(kv, q, z, other, n):
     # the exponential, the logarithm of the sum (at most 2) and the sum of two heads; the exponent's rounding
     tol = (2.0**-20 + 2.0**-24 * (z - other + 2)) * want
     assert np.all(np.abs(f64(scores)[0, 0] - want) <= tol), (f64(scores)[0, 0][[7, 100, n - 3]], want[[7, 100, n - 3]])
+
+
+# ---------------------------------------------------------------- e4m3 pages under queries of any size
+
+
+@pytest.mark.parametrize("top", [2.0**127, 2.0**126, 2.0**-113, 2.0**-125])
+def test_e4m3_queries_at_the_ends_of_bf16(top):
+    """bf16 queries whose largest value has the greatest exponents there are, or the least: their
+    products with the keys are in fp32's range, so the scores are finite and count."""
+    c = Case([300], hq=2, hkv=1, d=64, page=64, kv="e4m3", q="bf16", seed=5, k_scale=2.0**-60 if top > 1 else 2.0**60)
+    r = c.randn(c.pool, 1, 64, 64).sign()
+    at = -9 if top > 1 else 4  # stored keys: the least there are, or large ones
+    k = torch.where(torch.arange(64) < 2, r * 2.0 ** torch.randint(at, at + 4, r.shape, generator=c.g), 0.0)
+    c.k, c.v = c.put(k), c.put(c.randn(c.pool, 1, 64, 64))
+    x = torch.zeros(1, 2, 64)
+    x[..., 0], x[..., 1] = top, top / 2
+    x = x.to(c.qt).to(c.device)
+    sm = 1.0 / (float(x.max()) * c.k_scale * 2.0 ** (at + 2))  # scores of up to a few units
+    out, lse = c.cache().decode(x, c.ints([300]), sm_scale=sm, return_lse=True)
+    check_decode(c, x, out, lse, [(0, np.arange(300))], scale=float(np.float32(sm)))
