@@ -78,9 +78,10 @@ typedef struct {
  * q_out[t] = z of q; the page receives z of k divided by k_scale and v divided by v_scale (e4m3
  * saturates at 448).  positions: DEVICE [n_tokens], NULL: a token's slot (of a cache that evicts,
  * slots are not positions).  slot_pos: DEVICE [n_seqs][Hkv][slot_pos_stride] or NULL, receives
- * each new slot's position.  With kv->bounds, a page whose slot 0 is written starts its bounds
- * from this call's keys; other pages' bounds are widened by them.  (After dropping tokens from a
- * page, its bounds stay valid but wide until rtp_paged_bounds.)
+ * each new slot's position.  Of a token whose slot lies outside the table, and of all tokens of a
+ * sequence of negative length, q alone is taken.  With kv->bounds, a page whose slot 0 is written
+ * starts its bounds from this call's keys; other pages' bounds are widened by them.  (After dropping
+ * tokens from a page, its bounds stay valid but wide until rtp_paged_bounds.)
  *
  * q, k, v: DEVICE fp16 or bf16 (dtype; that of the pages unless those are e4m3), heads
  * contiguous, rows q_stride, k_stride, v_stride elements apart (multiples of 8).  q_out: rows

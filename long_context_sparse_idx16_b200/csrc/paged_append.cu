@@ -218,11 +218,13 @@ __global__ void __launch_bounds__(32 * kWarps, 5) append_kernel(const AppendArgs
   uint4 x[U][2];
 #pragma unroll
   for (int n = 0; n < U; ++n) load(u0 + n, x[n]);
-  const int64_t slot = (int64_t)a.seq_len[b] + i;
+  const int start = a.seq_len[b];
+  const int64_t slot = (int64_t)start + i;
   const int pos = a.positions ? a.positions[t] : (int)slot;
   int64_t page = -1;
   if (u1 > gq) {
-    if (slot >= 0 && slot < ((int64_t)kv.max_pages << kv.page_shift))
+    // (a negative length takes out all of its sequence: tokens behind it would land on older ones)
+    if (start >= 0 && slot < ((int64_t)kv.max_pages << kv.page_shift))
       page = paged_page(kv, b, (int)(slot >> kv.page_shift));
     if (page < 0 && lane == 0) paged_err(kv, RTP_PAGED_ERANGE);
   }

@@ -105,3 +105,42 @@ def test_e4m3_queries_at_the_ends_of_bf16(top):
     sm = 1.0 / (float(x.max()) * c.k_scale * 2.0 ** (at + 2))  # scores of up to a few units
     out, lse = c.cache().decode(x, c.ints([300]), sm_scale=sm, return_lse=True)
     check_decode(c, x, out, lse, [(0, np.arange(300))], scale=float(np.float32(sm)))
+
+
+# ---------------------------------------------------------------- append
+
+
+def chunk(c, T):
+    return [c.randn(T, h, c.d).to(c.qt).to(c.device) for h in (c.hq, c.hkv, c.hkv)]
+
+
+def same_pages(c, k0, v0):
+    return np.array_equal(f64(c.k), k0, equal_nan=True) and np.array_equal(f64(c.v), v0, equal_nan=True)
+
+
+def test_append_leaves_out_a_sequence_of_negative_length():
+    """All of its tokens, not only those whose slot is negative; the sequence beside it is written."""
+    from long_context_sparse_idx16_b200 import RTPError
+
+    c = Case([20, 33], hq=2, hkv=1, d=64, page=16, kv="fp16", room=8, seed=2)
+    bounds = torch.zeros((c.pool, 1, 2, 64), dtype=c.kt, device=c.device)
+    slots = torch.full((2, 1, c.width * 16), -1, dtype=torch.int32, device=c.device)
+    cache = c.cache(bounds=bounds)
+    cache.update_bounds(c.ints(c.lens))
+    q, k, v = chunk(c, 6)
+    k0, v0, b0 = f64(c.k), f64(c.v), f64(bounds)
+    cache.append(q, k, v, c.ints([-1, 33]), cu_new=c.ints([0, 4, 6]), slot_positions=slots)
+    with pytest.raises(RTPError):
+        cache.check()
+    page, rows = int(c.table[1, 2]), slice(1, 3)
+    for x, y in ((f64(c.k), k0), (f64(c.v), v0)):
+        assert not np.isnan(x[page, :, rows]).any()
+        y[page, :, rows] = x[page, :, rows]
+    assert same_pages(c, k0, v0)
+    want = np.full(slots.shape, -1)
+    want[1, 0, 33:35] = [33, 34]
+    assert np.array_equal(slots.cpu().numpy(), want)
+    got = f64(bounds)
+    assert np.array_equal(got[page, 0, 0], f64(c.k)[page, 0, :3].min(0))
+    b0[page] = got[page]
+    assert np.array_equal(got, b0)
