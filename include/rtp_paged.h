@@ -20,7 +20,7 @@
  *     into a graph.  Lengths and tables are read on the device: a captured call follows them.
  *   - Argument errors are found on the host before any launch: RTP_EINVAL, no side effects,
  *     rtp_last_error(NULL) says what.  Errors that only the device can see (a page number outside
- *     the pool, a length outside the table, a sequence number outside the batch) never make a
+ *     the pool, a length outside the table, a sequence or row number outside the batch) never make a
  *     kernel read or write outside its arrays: what such an entry names is left out, and
  *     RTP_PAGED_ERANGE is set in the err word of rtp_paged_kv, if there is one.
  *   - Calls that share a workspace must not overlap on the GPU: one workspace per stream, and one
@@ -70,9 +70,10 @@ typedef struct {
 } rtp_paged_kv;
 
 /* Append new tokens.  Token t of sequence b is row cu_new[b] + i of q, k and v (cu_new DEVICE
- * [n_seqs + 1], ascending from 0, rows at and behind cu_new[n_seqs] are left alone; NULL: one
- * token per sequence, row b, n_tokens == n_seqs) and goes to slot seq_len[b] + i (seq_len: DEVICE, the lengths BEFORE the call).  For each head row x
- * of q and k, in fp32 and rounded once:
+ * [n_seqs + 1], ascending from 0; rows that no sequence names are left alone, RTP_PAGED_ERANGE tells
+ * of offsets that descend, begin elsewhere or pass n_tokens; NULL: one token per sequence, row b,
+ * n_tokens == n_seqs) and goes to slot seq_len[b] + i (seq_len: DEVICE, the lengths BEFORE the
+ * call).  For each head row x of q and k, in fp32 and rounded once:
  *     y = x / sqrt(mean(x^2) + eps) * weight      (weight NULL: y = x)
  *     z = y rotated by its position: pair (c, c + D/2) by position * rope_base^(-2c/D)
  * q_out[t] = z of q; the page receives z of k divided by k_scale and v divided by v_scale (e4m3

@@ -166,9 +166,9 @@ struct Range8 {
   }
 };
 
-// Sequence of token t: the last b with cu[b] <= t, or -1 behind the last sequence.  A warp looks at
-// 32 places at a time.
-__device__ __forceinline__ int token_seq(const int32_t* cu, int n_seqs, int t) {
+// Sequence of token t: the last b with cu[b] <= t, or -1 if no sequence names row t.  A warp looks at
+// 32 places at a time.  *first: cu[b].
+__device__ __forceinline__ int token_seq(const int32_t* cu, int n_seqs, int t, int* first) {
   int lo = 0, n = n_seqs + 1;  // the answer lies in [lo, lo + n)
   while (n > 32) {
     const int step = (n + 31) / 32, at = lo + (threadIdx.x & 31) * step;
@@ -177,10 +177,19 @@ __device__ __forceinline__ int token_seq(const int32_t* cu, int n_seqs, int t) {
     n = min(step, lo + n - (lo + k * step));
     lo += k * step;
   }
-  const int at = lo + (threadIdx.x & 31);
-  const uint32_t le = __ballot_sync(0xffffffffu, (threadIdx.x & 31) < n && cu[min(at, n_seqs)] <= t);
-  const int b = lo + 31 - __clz(le | 1u);
-  return b < n_seqs ? b : -1;
+  const int c = cu[min(lo + (int)(threadIdx.x & 31), n_seqs)];
+  const uint32_t le = __ballot_sync(0xffffffffu, (threadIdx.x & 31) < n && c <= t);
+  const int k = 31 - __clz(le | 1u);
+  *first = __shfl_sync(0xffffffffu, c, k);
+  return (le & 1u) && lo + k < n_seqs ? lo + k : -1;
+}
+
+// Offsets that begin elsewhere than at 0, descend or name more rows than there are; by one CTA.
+__device__ __forceinline__ void check_offsets(const int32_t* cu, int n_seqs, int n_tokens, uint32_t* err) {
+  bool bad = threadIdx.x == 0 && (cu[0] != 0 || cu[n_seqs] > n_tokens);
+#pragma unroll 4
+  for (int e = threadIdx.x; e < n_seqs; e += 32 * kWarps) bad |= cu[e] > cu[e + 1];
+  if (bad && err) atomicOr(err, RTP_PAGED_ERANGE);
 }
 
 // Row groups of a token: ceil(Hq / R) of q, then ceil(Hkv / R) of k, then as many of v; `run` of them
@@ -195,12 +204,14 @@ __global__ void __launch_bounds__(32 * kWarps, 5) append_kernel(const AppendArgs
   const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int t = (int)(task / runs), lane = threadIdx.x & 31, sub = lane / L, c = (lane % L) * 8;
   after_wait();
+  // (a CTA behind those of the tokens: inside theirs the test costs registers, and 2% of a large chunk)
+  if (a.cu_new && blockIdx.x == gridDim.x - 1) return check_offsets(a.cu_new, kv.n_seqs, a.n_tokens, kv.err);
   if (t >= a.n_tokens) return;
   int b = t, i = 0;
   if (a.cu_new) {
-    b = token_seq(a.cu_new, kv.n_seqs, t);
-    if (b < 0) return;  // rows behind the last sequence stay as they are
-    i = t - a.cu_new[b];
+    b = token_seq(a.cu_new, kv.n_seqs, t, &i);
+    if (b < 0) return;  // rows before the first sequence and behind the last stay as they are
+    i = t - i;
   }
   const int gq = (a.Hq + R - 1) / R, gk = (kv.Hkv + R - 1) / R;
   const int u0 = (int)(task % runs) * run, u1 = min(u0 + run, gq + 2 * gk);
@@ -223,8 +234,9 @@ __global__ void __launch_bounds__(32 * kWarps, 5) append_kernel(const AppendArgs
   const int pos = a.positions ? a.positions[t] : (int)slot;
   int64_t page = -1;
   if (u1 > gq) {
-    // (a negative length takes out all of its sequence: tokens behind it would land on older ones)
-    if (start >= 0 && slot < ((int64_t)kv.max_pages << kv.page_shift))
+    // (a negative length takes out all of its sequence: tokens behind it would land on older ones; i is
+    // negative where an offset so far below 0 overflows it)
+    if ((start | i) >= 0 && slot < ((int64_t)kv.max_pages << kv.page_shift))
       page = paged_page(kv, b, (int)(slot >> kv.page_shift));
     if (page < 0 && lane == 0) paged_err(kv, RTP_PAGED_ERANGE);
   }
@@ -384,10 +396,11 @@ __global__ void __launch_bounds__(kBoundThreads) append_bounds_kernel(const Appe
   const PagedView& kv = a.kv;
   const int b = blockIdx.z;
   // (the lengths and the table are inputs of the whole operator: read ahead)
-  const int n = a.cu_new[b + 1] - a.cu_new[b];
-  const int64_t cap = (int64_t)kv.max_pages << kv.page_shift;
-  const int64_t s0 = a.seq_len[b], s1 = min(s0 + n, cap);
-  if (s0 < 0 || s0 >= s1) return after_wait();
+  const int64_t cap = (int64_t)kv.max_pages << kv.page_shift, start = a.seq_len[b];
+  // the slots of the rows that were given
+  const int64_t row0 = a.cu_new[b], row1 = a.cu_new[b + 1];
+  const int64_t s0 = start + max(row0, (int64_t)0) - row0, s1 = min(start + min(row1, (int64_t)a.n_tokens) - row0, cap);
+  if (start < 0 || s0 >= s1) return after_wait();
   bool waited = false;
   for (int64_t i = (s0 >> kv.page_shift) + blockIdx.x; i << kv.page_shift < s1; i += gridDim.x) {
     const int64_t base = i << kv.page_shift, first = max(s0, base), last = min(s1, base + kv.page_size);
@@ -424,7 +437,7 @@ cudaError_t run_append(const AppendArgs& a, cudaStream_t st) {
   const int runs = (groups + run - 1) / run;
   const int64_t warps = (int64_t)a.n_tokens * runs;
   const bool one = !a.cu_new && a.kv.bounds;
-  const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps));
+  const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps + (a.cu_new ? 1 : 0)));
   const cudaError_t e = run == 1 ? launch_after(append_kernel<T, K, D, 1>, grid, 32 * kWarps, 0, st, a, run, runs, one)
                                  : launch_after(append_kernel<T, K, D, 2>, grid, 32 * kWarps, 0, st, a, run, runs, one);
   if (e != cudaSuccess || !a.kv.bounds || one) return e;

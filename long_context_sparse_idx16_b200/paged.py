@@ -38,12 +38,13 @@ class PagedKV(_paged.PagedKV):
            k_weight=None, eps=1e-6, rope_base=1e6, q_out=None, slot_positions=None, stream=None)
         Append new tokens: norm and rotate q and k per head, write k and v to their pages.
         q: [T][Hq][D] or None; k, v: [T][Hkv][D] (rows may be slices of one projection's output).
-        seq_lens: int32 [n_seqs], the lengths before the call.  cu_new: int32 [n_seqs + 1], the rows
-        of each sequence (None: one token for each; rows behind the last are left alone); max_new:
-        about the most tokens of one sequence (default T, sizes a launch).  positions: int32 [T] (default: each token's slot).  q_weight, k_weight: [D]
-        norm weights in the activations' dtype (None: no norm).  slot_positions: int32
-        [n_seqs][Hkv][S], receives the position of each new slot.  Returns q_out ([T][Hq][D], which
-        may be q itself), or None without q.  The caller advances its lengths.
+        seq_lens: int32 [n_seqs], the lengths before the call.  cu_new: int32 [n_seqs + 1], ascending
+        from 0, the rows of each sequence (None: one token for each; rows behind the last are left
+        alone); max_new: about the most tokens of one sequence (default T, sizes a launch).
+        positions: int32 [T] (default: each token's slot).  q_weight, k_weight: [D] norm weights in
+        the activations' dtype (None: no norm).  slot_positions: int32 [n_seqs][Hkv][S], receives the
+        position of each new slot.  Returns q_out ([T][Hq][D], which may be q itself), or None
+        without q.  The caller advances its lengths.
 
     decode(q, seq_lens, *, row_seq=None, window=0, n_sink=0, sm_scale=0, pages=None, scores=None,
            out=None, return_lse=False, stream=None)

@@ -144,3 +144,48 @@ def test_append_leaves_out_a_sequence_of_negative_length():
     assert np.array_equal(got[page, 0, 0], f64(c.k)[page, 0, :3].min(0))
     b0[page] = got[page]
     assert np.array_equal(got, b0)
+
+
+@pytest.mark.parametrize("cu,rows,written", [
+    ([0, 3, 9], 6, {0: 3, 1: 3}),        # the last sequence names rows that were not given
+    ([0, 3, 1 << 30], 6, {0: 3, 1: 3}),
+    ([2, 5, 6], 6, {0: 3, 1: 1}),        # rows before the first sequence
+    ([-(2**31), 3, 6], 6, {1: 3}),       # tokens numbered beyond 32 bits
+    ([-2, 3, 6], 6, {0: 3, 1: 3})])      # the first sequence's tokens 2, 3, 4, behind two that were not given
+def test_append_row_offsets_outside_the_rows(cu, rows, written):
+    """Only rows that are there and named are written, to the slots of their tokens; the page bounds
+    enclose what the pages hold and nothing else, and the caller hears of it."""
+    from long_context_sparse_idx16_b200 import RTPError
+
+    c = Case([18, 33], hq=2, hkv=1, d=64, page=16, kv="fp16", room=16, seed=3)
+    bounds = torch.zeros((c.pool, 1, 2, 64), dtype=c.kt, device=c.device)
+    cache = c.cache(bounds=bounds)
+    cache.update_bounds(c.ints(c.lens))
+    q, k, v = chunk(c, rows)
+    # what no sequence has written would show in the bounds
+    kk = torch.nan_to_num(c.k, nan=100.0)
+    c.k.copy_(kk)
+    k0, b0 = f64(c.k), f64(bounds)
+    out = torch.full_like(q, 9.0)
+    cache.append(q, k, v, c.ints(c.lens), cu_new=c.ints(cu), q_out=out, max_new=rows)
+    with pytest.raises(RTPError):
+        cache.check()
+    got, lim = f64(c.k), f64(bounds)
+    touched = {}
+    for b, n in written.items():
+        first = max(cu[b], 0)
+        for t in range(first, first + n):
+            s = c.lens[b] + t - cu[b]
+            p, o = int(c.table[b, s // 16]), s % 16
+            assert np.all(np.abs(got[p, 0, o]) < 50) and not np.array_equal(got[p, 0, o], k0[p, 0, o])
+            k0[p, 0, o] = got[p, 0, o]
+            touched.setdefault((p, s // 16 * 16 < c.lens[b]), []).append(o)
+    assert np.array_equal(got, k0)
+    for (p, widened), o in touched.items():
+        lo, hi = got[p, 0, o].min(0), got[p, 0, o].max(0)
+        if widened:
+            lo, hi = np.minimum(lo, b0[p, 0, 0]), np.maximum(hi, b0[p, 0, 1])
+        assert np.array_equal(lim[p, 0, 0], lo) and np.array_equal(lim[p, 0, 1], hi)
+        b0[p] = lim[p]
+    assert np.array_equal(lim, b0)
+    assert bool((out[:max(cu[0], 0)] == 9.0).all())
