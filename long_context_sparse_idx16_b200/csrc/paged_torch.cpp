@@ -126,9 +126,10 @@ class PagedKV {
     if (q) {
       qs = heads(*q, "q", T, -1, &dt);
       hq = q->size(1);
-      if (!q_out) q_out = make({T, hq, h_.head_dim}, dt);
+      if (!q_out) q_out = make(guard, {T, hq, h_.head_dim}, dt);
       os = heads(*q_out, "q_out", T, hq, &dt);
     }
+    guard.inputs(*this, q, k, v, seq_lens, cu_new, positions, q_weight, k_weight, q_out, slot_positions);
     if (T)
       check(rtp_paged_append(&h_, ptr(q), k.data_ptr(), v.data_ptr(), code_of(dt), qs, ks, vs, num(T), num(hq),
                              static_cast<int32_t*>(ptr(cu_new)), num(max_new.value_or(T)), seq_lens.data_ptr<int32_t>(),
@@ -141,6 +142,7 @@ class PagedKV {
     if (!bounds_) bad("the cache keeps no page bounds");
     exact(seq_lens, "seq_lens", {h_.n_seqs}, at::kInt);
     const Guard guard(*this, stream);
+    guard.inputs(*this, seq_lens);
     check(rtp_paged_bounds(&h_, seq_lens.data_ptr<int32_t>(), guard.stream));
   }
 
@@ -165,10 +167,12 @@ class PagedKV {
     if (scores) st = slots(*scores, "scores", at::kFloat);
     const at::ScalarType dt = q.scalar_type();
     const Guard guard(*this, stream);
-    if (!out) out = make({n, hq, h_.head_dim}, dt);
+    if (!out) out = make(guard, {n, hq, h_.head_dim}, dt);
     const int64_t os = heads(*out, "out", n, hq, &dt);
     OptTensor lse;
-    if (return_lse) lse = make({n, hq}, at::kFloat);
+    if (return_lse) lse = make(guard, {n, hq}, at::kFloat);
+    guard.inputs(*this, q, seq_lens, row_seq, scores, out);
+    if (pages) guard.inputs(*this, pages->first, pages->second);
     if (n) {
       const size_t need = rtp_paged_decode_workspace(&h_, num(n), num(hq), scores ? 1 : 0);
       const at::DataPtr ws = workspace(need);
@@ -188,8 +192,9 @@ class PagedKV {
     if (!bounds_) bad("the cache keeps no page bounds");
     if (top_pages < 1) bad("top_pages must be at least 1");
     const Guard guard(*this, stream);
-    const Tensor sel = make({n, h_.n_kv_heads, top_pages}, at::kInt);
-    const Tensor cnt = make({n, h_.n_kv_heads}, at::kInt);
+    const Tensor sel = make(guard, {n, h_.n_kv_heads, top_pages}, at::kInt);
+    const Tensor cnt = make(guard, {n, h_.n_kv_heads}, at::kInt);
+    guard.inputs(*this, q, seq_lens, row_seq);
     if (n) {
       const size_t need = rtp_paged_select_workspace(&h_, num(n), num(hq));
       const at::DataPtr ws = workspace(need);
@@ -211,7 +216,8 @@ class PagedKV {
                                       std::tuple{&po, "out_positions", at::kInt}})
       if (slots(*t, name, dt) != st) bad(name, ": expected ", std::to_string(st), " slots, as scores have");
     const Guard guard(*this, stream);
-    const Tensor len = make({h_.n_seqs}, at::kInt);
+    const Tensor len = make(guard, {h_.n_seqs}, at::kInt);
+    guard.inputs(*this, seq_lens, scores, positions, so, po);
     const size_t need = rtp_paged_evict_workspace(&h_, st);
     const at::DataPtr ws = workspace(need);
     check(rtp_paged_evict(&h_, seq_lens.data_ptr<int32_t>(), num(budget), num(n_recent), num(n_sink),
@@ -230,20 +236,48 @@ class PagedKV {
   }
 
  private:
-  // The cache's device, and the stream that the call (and what it allocates) uses.
+  // The cache's device, and the stream that the call (and what it allocates) uses.  If that is not the
+  // current one, torch's allocator is told of every tensor that crosses: a tensor freed after the call
+  // would otherwise go to work of the one stream while the other still reads it.
   struct Guard {
     c10::OptionalDeviceGuard device;
     c10::OptionalStreamGuard other;
+    std::optional<c10::Stream> mine, callers;  // with a stream given that is not the current one
     cudaStream_t stream = nullptr;
     Guard(const PagedKV& kv, const py::object& s) {
       if (!kv.device_.is_cuda()) bad("the cache must be on a CUDA device, not ", kv.device_.str());
       device.reset_device(kv.device_);
+      const at::cuda::CUDAStream current = at::cuda::getCurrentCUDAStream(kv.device_.index());
+      stream = current.stream();
       if (!s.is_none()) {
         const c10::Stream st = stream_of(s);
         if (st.device() != kv.device_) bad("stream: expected a stream of ", kv.device_.str());
-        other.reset_stream(st);
+        if (st != current.unwrap()) {
+          other.reset_stream(st);
+          mine = st;
+          callers = current.unwrap();
+          stream = at::cuda::getCurrentCUDAStream(kv.device_.index()).stream();
+        }
       }
-      stream = at::cuda::getCurrentCUDAStream(kv.device_.index()).stream();
+    }
+    template <typename... T>
+    void inputs(const PagedKV& kv, const T&... t) const {
+      if (!mine) return;
+      (read(t), ...);
+      read(kv.k_);
+      read(kv.v_);
+      read(kv.table_);
+      read(kv.bounds_);
+      read(kv.err_);
+    }
+    void output(const Tensor& t) const {
+      if (mine) t.record_stream(*callers);
+    }
+
+   private:
+    void read(const Tensor& t) const { t.record_stream(*mine); }
+    void read(const OptTensor& t) const {
+      if (t) t->record_stream(*mine);
     }
   };
 
@@ -255,8 +289,10 @@ class PagedKV {
   // A new tensor, and a workspace that lives until the call returns (its memory is then torch's to give
   // to later work of the same stream).  Both straight from torch's allocator: through the dispatcher an
   // allocation takes 0.5 us more, and a decode call makes three.
-  Tensor make(at::IntArrayRef shape, at::ScalarType dt) const {
-    return at::detail::empty_cuda(shape, dt, device_, std::nullopt);
+  Tensor make(const Guard& guard, at::IntArrayRef shape, at::ScalarType dt) const {
+    const Tensor t = at::detail::empty_cuda(shape, dt, device_, std::nullopt);
+    guard.output(t);
+    return t;
   }
   static at::DataPtr workspace(size_t n) {
     return c10::cuda::CUDACachingAllocator::get()->allocate(std::max<size_t>(n, 16));

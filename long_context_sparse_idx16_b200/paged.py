@@ -31,7 +31,9 @@ class PagedKV(_paged.PagedKV):
 
     Methods are asynchronous on ``stream`` (default: the current stream of the cache's device) and
     can be captured into a CUDA graph.  Outputs and workspaces come from torch's allocator, on that
-    stream, for each call.  What only the device can see wrong (a page number outside the pool, a
+    stream, for each call.  With a stream other than the current one, the caller makes it wait for the
+    work that the inputs come from, and the current one for the results; tensors may be dropped on either
+    side as soon as the call has returned.  What only the device can see wrong (a page number outside the pool, a
     length outside the table) is left out of the result and reported by ``check()``.
 
     append(q, k, v, seq_lens, *, cu_new=None, max_new=None, positions=None, q_weight=None,

@@ -189,3 +189,122 @@ def test_append_row_offsets_outside_the_rows(cu, rows, written):
         b0[p] = lim[p]
     assert np.array_equal(lim, b0)
     assert bool((out[:max(cu[0], 0)] == 9.0).all())
+
+
+# ---------------------------------------------------------------- streams and threads
+
+
+def busy(stream, cycles=200_000_000):
+    """About 0.1 s of a kernel that only counts, on `stream`."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(cycles)
+
+
+def overwrite(*like):
+    """What later work of the current stream does with memory that was freed to it: ones everywhere."""
+    return [torch.empty_like(x).fill_(1) for x in like for _ in range(6)]
+
+
+def test_temporaries_given_to_another_stream():
+    """Inputs that nobody holds once the call has returned: the stream that reads them later still finds
+    them, whatever the current stream allocates meanwhile."""
+    from long_context_sparse_idx16_b200 import RTPError
+
+    c = Case([3000, 900], hq=8, hkv=2, d=128, page=64, kv="fp16", seed=31, room=70)
+    lens = c.ints(c.lens)
+    q = c.randn(2, 8, 128).to(c.qt).to(c.device)
+    kn, vn = (c.randn(2, 2, 128).to(c.qt).to(c.device) for _ in "kv")
+    bounds = torch.zeros((c.pool, 2, 2, 128), dtype=c.kt, device=c.device)
+    cache = c.cache(bounds=bounds)
+    cache.update_bounds(lens)
+    k0, v0, b0 = c.k.clone(), c.v.clone(), bounds.clone()
+    drawn = torch.rand((2, 2, cache.capacity), device=c.device)
+    pos = torch.arange(cache.capacity, dtype=torch.int32, device=c.device).expand(2, 2, -1).contiguous()
+    cu, seq = c.ints([0, 1, 2]), c.ints([1, 0])
+    side = torch.cuda.Stream()
+
+    def reset():
+        c.k.copy_(k0), c.v.copy_(v0), bounds.copy_(b0)
+
+    def steps(kw, t):
+        """Each call and its result; t makes the inputs it is given."""
+        yield lambda: (cache.append(t(q), t(kn), t(vn), t(lens), cu_new=t(cu), positions=t(lens), **kw), c.k, c.v, bounds)
+        yield lambda: (cache.update_bounds(t(lens + 1), **kw), bounds)[1:]
+        yield lambda: (cache.decode(t(q), t(lens), **kw),)
+        yield lambda: (cache.decode(t(q), t(lens), row_seq=t(seq), **kw),)
+        yield lambda: cache.select_pages(t(q), t(lens), 5, row_seq=t(seq), **kw)
+        yield lambda: (cache.decode(t(q), t(lens), pages=tuple(t(x) for x in sel), **kw),)
+        yield lambda: (*cache.evict(t(lens), 500, t(drawn), t(pos), n_recent=9, **kw), c.k, c.v)
+
+    sel = cache.select_pages(q, lens, 5)
+    want = []
+    for f in steps({}, lambda x: x):
+        d0, p0 = drawn.clone(), pos.clone()
+        reset()
+        want.append([x.clone() for x in f()])
+        drawn.copy_(d0), pos.copy_(p0)
+
+    def temporary(x):
+        y = x.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        return y
+
+    for i, f in enumerate(steps(dict(stream=side), temporary)):
+        reset()
+        torch.cuda.synchronize()
+        busy(side)
+        got = f()
+        held = overwrite(q, kn, lens, cu, seq, drawn, pos, *sel)
+        torch.cuda.synchronize()
+        del held
+        for a, b in zip(got, want[i]):
+            a, b = (x.nan_to_num(7.0) if x.is_floating_point() else x for x in (a, b))
+            assert torch.equal(a, b), i
+    with pytest.raises(RTPError):  # row_seq names 3000 slots of the sequence that has pages for 970
+        cache.check()
+
+
+def test_a_cache_dropped_while_another_stream_reads_it():
+    c = Case([3000], hq=8, hkv=2, d=128, page=64, kv="fp16", seed=32)
+    lens, q = c.ints(c.lens), c.randn(1, 8, 128).to(c.qt).to(c.device)
+    want = c.cache().decode(q, lens)
+    side = torch.cuda.Stream()
+    k, v, table = c.k.clone(), c.v.clone(), c.table.to(c.device)
+    torch.cuda.synchronize()
+    busy(side)
+    side.wait_stream(torch.cuda.current_stream())
+    from long_context_sparse_idx16_b200 import PagedKV
+
+    cache = PagedKV(k, v, table)
+    del k, v, table
+    out = cache.decode(q, lens, stream=side)
+    del cache
+    held = overwrite(c.k, c.table.to(c.device))
+    torch.cuda.synchronize()
+    del held
+    assert torch.equal(out, want)
+
+
+def test_results_dropped_while_the_current_stream_reads_them():
+    """A result of another stream, dropped when its reader is enqueued, is not given to that stream's next
+    call before the reader is done."""
+    c = Case([300], hq=8, hkv=2, d=128, page=64, kv="fp16", seed=33)
+    lens = c.ints(c.lens)
+    q = [c.randn(1, 8, 128).to(c.qt).to(c.device) for _ in range(2)]
+    bounds = torch.zeros((c.pool, 2, 2, 128), dtype=c.kt, device=c.device)
+    cache = c.cache(bounds=bounds)
+    cache.update_bounds(lens)
+    calls = [lambda q, **kw: cache.decode(q, lens, return_lse=True, **kw), lambda q, **kw: cache.select_pages(q, lens, 3, **kw),
+             lambda q, **kw: (cache.append(q, q[:, :2], q[:, 2:4], lens - 1, **kw),)]
+    side, now = torch.cuda.Stream(), torch.cuda.current_stream()
+    for f in calls:
+        want = [x.clone() for x in f(q[0])]
+        torch.cuda.synchronize()
+        got = f(q[0], stream=side)
+        now.wait_stream(side)
+        busy(now)
+        copies = [x.clone() for x in got]
+        del got
+        f(q[1], stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(copies, want))
