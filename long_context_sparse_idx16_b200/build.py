@@ -54,7 +54,7 @@ def build_binding(force: bool = False) -> str:
     cmd += ["-o", EXT, EXT_SOURCE, "-L", PKG, "-l:librtp.so", "-Wl,-rpath,$ORIGIN"]
     for d in ce.library_paths("cuda"):
         cmd += ["-L", d]
-    cmd += ["-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    cmd += ["-lc10", "-lc10_cuda", "-lcudart", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     subprocess.check_call(cmd)
     return EXT
 

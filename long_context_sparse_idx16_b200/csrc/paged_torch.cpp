@@ -6,9 +6,13 @@
 #include <ATen/cuda/CUDAContext.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/extension.h>
 
+#include <map>
+#include <mutex>
 #include <optional>
 #include <string>
 
@@ -52,6 +56,40 @@ c10::Stream stream_of(const py::object& s) {
                               (c10::DeviceType)s.attr("device_type").cast<int64_t>());
 }
 
+// A zero in the device's memory for a cache's errors.  It is zero when this returns, whatever the streams
+// still have to do (a memset on the current stream would come behind the first errors of another), and
+// is never given back: kernels of a cache that was dropped may still write it.  Four bytes a cache.
+uint32_t* error_word(int device) {
+  constexpr int kWords = 1 << 14;
+  struct Slab {
+    uint32_t* next = nullptr;
+    int left = 0;
+  };
+  static std::mutex lock;
+  static std::map<int, Slab>& slabs = *new std::map<int, Slab>;
+  const std::lock_guard<std::mutex> held(lock);
+  Slab& s = slabs[device];
+  if (!s.left) {
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+    const c10::cuda::CUDAStreamCaptureModeGuard relaxed(cudaStreamCaptureModeRelaxed);  // a capture may be under way
+    void* p = nullptr;
+    if (cudaMalloc(&p, kWords * sizeof(uint32_t)) != cudaSuccess) {
+      cudaGetLastError();
+      c10::cuda::CUDACachingAllocator::emptyCache();
+      C10_CUDA_CHECK(cudaMalloc(&p, kWords * sizeof(uint32_t)));
+    }
+    cudaStream_t st;
+    C10_CUDA_CHECK(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking));
+    C10_CUDA_CHECK(cudaMemsetAsync(p, 0, kWords * sizeof(uint32_t), st));
+    C10_CUDA_CHECK(cudaStreamSynchronize(st));
+    C10_CUDA_CHECK(cudaStreamDestroy(st));
+    s.next = static_cast<uint32_t*>(p);
+    s.left = kWords;
+  }
+  --s.left;
+  return s.next++;
+}
+
 class PagedKV {
  public:
   PagedKV(const Tensor& k, const Tensor& v, const Tensor& table, double k_scale, double v_scale, const OptTensor& bounds)
@@ -87,15 +125,13 @@ class PagedKV {
       exact(*bounds, "bounds", {k.size(0), k.size(1), 2, k.size(3)}, dtype_);
       h_.bounds = bounds->data_ptr();
     }
-    err_ = at::zeros({1}, at::TensorOptions().dtype(at::kInt).device(device_));
-    h_.err = reinterpret_cast<uint32_t*>(err_.data_ptr<int32_t>());
+    if (device_.is_cuda()) h_.err = error_word(device_.index());
   }
 
   const Tensor& k() const { return k_; }
   const Tensor& v() const { return v_; }
   const Tensor& table() const { return table_; }
   const OptTensor& bounds() const { return bounds_; }
-  const Tensor& err() const { return err_; }
   py::object device() const { return py::cast(device_); }
   int64_t n_seqs() const { return h_.n_seqs; }
   int64_t n_pages() const { return h_.n_pages; }
@@ -230,8 +266,9 @@ class PagedKV {
   // Bits of the error word, cleared; waits for the stream.
   int64_t errors(const py::object& stream) {
     const Guard guard(*this, stream);
-    const int64_t w = err_.item<int32_t>();
-    if (w) err_.zero_();
+    uint32_t w = 0;
+    c10::cuda::memcpy_and_sync(&w, h_.err, sizeof(w), cudaMemcpyDeviceToHost, guard.stream);
+    if (w) C10_CUDA_CHECK(cudaMemsetAsync(h_.err, 0, sizeof(w), guard.stream));
     return w;
   }
 
@@ -268,7 +305,6 @@ class PagedKV {
       read(kv.v_);
       read(kv.table_);
       read(kv.bounds_);
-      read(kv.err_);
     }
     void output(const Tensor& t) const {
       if (mine) t.record_stream(*callers);
@@ -358,7 +394,7 @@ class PagedKV {
   }
 
   rtp_paged_kv h_{};
-  Tensor k_, v_, table_, err_;
+  Tensor k_, v_, table_;
   OptTensor bounds_;
   c10::Device device_;
   at::ScalarType dtype_;

@@ -308,3 +308,25 @@ def test_results_dropped_while_the_current_stream_reads_them():
         f(q[1], stream=side)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(copies, want))
+
+
+def test_errors_of_another_stream_are_kept():
+    """The error word is ready when the constructor returns, whatever the current stream still has to do."""
+    from long_context_sparse_idx16_b200 import RTPError
+
+    c = Case([300], hq=4, hkv=2, d=128, page=64, kv="fp16", seed=12)
+    q = c.randn(1, 4, 128).to(c.qt).to(c.device)
+    c.table[0, 1] = -5
+    lens, table = c.ints([300]), c.table.to(c.device)
+    side = torch.cuda.Stream()
+    from long_context_sparse_idx16_b200 import PagedKV
+
+    torch.cuda.synchronize()
+    busy(torch.cuda.current_stream())
+    cache = PagedKV(c.k, c.v, table)
+    cache.decode(q, lens, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    with pytest.raises(RTPError):
+        cache.check()
+    cache.check()
