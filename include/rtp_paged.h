@@ -13,6 +13,7 @@
  *                      with sinks, or a list of pages), split over the length and joined
  *   rtp_paged_select   the pages a query attends to, by an upper bound of its scores in each page
  *   rtp_paged_evict    a cache brought back to a budget by the attention weight its slots drew
+ *   rtp_paged_take_errors   what the kernels had to leave out since the last look
  *
  * Conventions shared by every entry point
  *   - Device pointers are plain addresses on the current device; every call is asynchronous and
@@ -68,6 +69,10 @@ typedef struct {
                                  page in each dimension; NULL: not kept */
   uint32_t* err;              /* DEVICE error word, or NULL */
 } rtp_paged_kv;
+
+/* Move kv->err to *bits (DEVICE) and clear it, in one step: an error that another stream reports
+ * meanwhile is in this answer or in the next. */
+rtp_status rtp_paged_take_errors(const rtp_paged_kv* kv, uint32_t* bits, cudaStream_t stream);
 
 /* Append new tokens.  Token t of sequence b is row cu_new[b] + i of q, k and v (cu_new DEVICE
  * [n_seqs + 1], ascending from 0; rows that no sequence names are left alone, RTP_PAGED_ERANGE tells

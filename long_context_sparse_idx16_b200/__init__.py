@@ -122,6 +122,7 @@ def lib() -> C.CDLL:
             "rtp_get_clusters": ([P, C.POINTER(rtp_cluster_view)], C.c_int),
             "rtp_paged_append": ([K, P, P, P, i32, i64, i64, i64, i32, i32, P, i32, P, P, P, P, f32, C.c_double, P,
                                   i64, P, i64, P], C.c_int),
+            "rtp_paged_take_errors": ([K, P, P], C.c_int),
             "rtp_paged_bounds": ([K, P, P], C.c_int),
             "rtp_paged_decode": ([K, P, i32, i64, i32, i32, P, P, i32, i32, f32, P, P, i64, P, i64, P, P, i64, P,
                                   C.c_size_t, P], C.c_int),

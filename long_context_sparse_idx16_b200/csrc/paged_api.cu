@@ -95,9 +95,20 @@ const char* check_rows(const rtp_paged_kv* kv, const void* q, int64_t q_stride, 
   return nullptr;
 }
 
+__global__ void take_errors_kernel(uint32_t* err, uint32_t* bits) { *bits = atomicExch(err, 0u); }
+
 }  // namespace
 
 extern "C" {
+
+rtp_status rtp_paged_take_errors(const rtp_paged_kv* kv, uint32_t* bits, cudaStream_t stream) {
+  const char* fn = "rtp_paged_take_errors";
+  if (const char* m = view_of(kv, nullptr)) return bad(fn, m);
+  if (!kv->err || !bits) return bad(fn, "kv->err and bits must not be NULL");
+  take_errors_kernel<<<1, 1, 0, stream>>>(kv->err, bits);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? RTP_OK : cuda_fail(nullptr, e, fn);
+}
 
 rtp_status rtp_paged_append(const rtp_paged_kv* kv, const void* q, const void* k, const void* v, int32_t dtype,
                             int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_tokens,

@@ -263,12 +263,15 @@ class PagedKV {
     return py::make_tuple(len, so, po);
   }
 
-  // Bits of the error word, cleared; waits for the stream.
+  // Bits of the error word, taken and cleared in one step; waits for the stream, and lets other Python
+  // threads (and host callbacks on the stream that need the interpreter) run meanwhile.
   int64_t errors(const py::object& stream) {
     const Guard guard(*this, stream);
+    const at::DataPtr bits = workspace(sizeof(uint32_t));
+    check(rtp_paged_take_errors(&h_, static_cast<uint32_t*>(bits.get()), guard.stream));
     uint32_t w = 0;
-    c10::cuda::memcpy_and_sync(&w, h_.err, sizeof(w), cudaMemcpyDeviceToHost, guard.stream);
-    if (w) C10_CUDA_CHECK(cudaMemsetAsync(h_.err, 0, sizeof(w), guard.stream));
+    const py::gil_scoped_release others;
+    c10::cuda::memcpy_and_sync(&w, bits.get(), sizeof(w), cudaMemcpyDeviceToHost, guard.stream);
     return w;
   }
 

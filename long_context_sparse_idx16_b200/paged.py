@@ -82,6 +82,6 @@ class PagedKV(_paged.PagedKV):
         if w & _ETIMEOUT:
             raise RTPError(RTP_ETIMEOUT, "a bounded in-kernel wait gave up")
         if w & _ERANGE:
-            raise RTPError(RTP_ERANGE, "a page, length or sequence number out of range was left out")
+            raise RTPError(RTP_ERANGE, "a page, length, sequence or row number out of range was left out")
         if w:
             raise RTPError(RTP_EINVAL, f"unknown device error {w}")

@@ -330,3 +330,58 @@ def test_errors_of_another_stream_are_kept():
     with pytest.raises(RTPError):
         cache.check()
     cache.check()
+
+
+def test_check_lets_other_threads_run():
+    """While check() waits for the GPU, another Python thread goes on."""
+    import threading
+    import time
+
+    c = Case([10], hq=2, hkv=1, d=64, page=16, kv="fp16", seed=1)
+    cache = c.cache()
+    cache.check()
+    torch.cuda.synchronize()
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.monotonic())
+            time.sleep(0.002)
+
+    t = threading.Thread(target=tick)
+    t.start()
+    time.sleep(0.02)
+    busy(torch.cuda.current_stream(), 1_000_000_000)  # half a second
+    began = time.monotonic()
+    cache.check()
+    ended = time.monotonic()
+    stop.set()
+    t.join()
+    assert ended - began > 0.2
+    inside = [x for x in ticks if began < x < ended - 0.05]
+    assert len(inside) > 10, len(inside)
+
+
+def test_errors_are_taken_once_and_none_is_lost():
+    """Two streams that report errors while a third takes them: every report is followed by an answer."""
+    from long_context_sparse_idx16_b200 import RTPError
+
+    c = Case([300], hq=4, hkv=2, d=128, page=64, kv="fp16", seed=12)
+    q = c.randn(1, 4, 128).to(c.qt).to(c.device)
+    c.table[0, 1] = -5
+    cache, lens = c.cache(), c.ints([300])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(50):
+        for s in streams[:2]:
+            cache.decode(q, lens, stream=s)
+        heard = 0
+        for last in (False, True):
+            if last:
+                torch.cuda.synchronize()
+            try:
+                cache.check(stream=streams[2])
+            except RTPError:
+                heard += 1
+        assert heard >= 1, i
+        cache.check()
