@@ -155,8 +155,8 @@ size_t rtp_paged_select_workspace(const rtp_paged_kv* kv, int32_t n_rows, int32_
  * score that is not a number ranks last).  Survivors in slots >= budget move into the freed slots
  * below it, in slot order: K and V rows, score, position; all other rows stay where they are, and
  * rows at and behind `budget` keep their bytes.  out_len[b] (DEVICE) = min(seq_len[b], budget);
- * out_scores and out_positions (may be scores and positions) receive slots 0 .. out_len - 1, then
- * 0 and -1 up to stride.  budget and stride are at most 2^24.  Pages moved into keep their bounds;
+ * out_scores and out_positions (may be scores and positions; no arrays share memory otherwise, so
+ * out_len is not seq_len) receive slots 0 .. out_len - 1, then 0 and -1 up to stride.  budget and stride are at most 2^24.  Pages moved into keep their bounds;
  * call rtp_paged_bounds where those are in use.  A page must belong to one sequence only. */
 rtp_status rtp_paged_evict(const rtp_paged_kv* kv, const int32_t* seq_len, int32_t budget, int32_t n_recent,
                            int32_t n_sink, const float* scores, const int32_t* positions, int64_t stride,

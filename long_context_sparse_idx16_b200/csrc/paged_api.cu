@@ -10,6 +10,12 @@ namespace {
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 int elem_size(int dtype) { return dtype == RTP_E4M3 ? 1 : 2; }
 
+// Whether two arrays share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + nb && y < x + na;
+}
+
 rtp_status bad(const char* fn, const char* what) { return fail(nullptr, RTP_EINVAL, std::string(fn) + ": " + what); }
 
 // Checks a cache description and fills the kernels' view of it; NULL if it is right, else what is not.
@@ -293,6 +299,19 @@ rtp_status rtp_paged_evict(const rtp_paged_kv* kv, const int32_t* seq_len, int32
     return bad(fn, "need n_sink + n_recent <= budget, none negative");
   if (stride < (int64_t)kv->max_pages * kv->page_size || stride > (1 << 24))
     return bad(fn, "stride must cover max_pages * page_size slots and be at most 2^24");
+  // CTAs of all heads read lengths, scores and positions while others have begun to write
+  const size_t lens = (size_t)kv->n_seqs * sizeof(int32_t), lists = lens * kv->n_kv_heads * stride;
+  if (overlap(out_len, lens, seq_len, lens)) return bad(fn, "out_len must not be seq_len");
+  if ((out_scores != scores && overlap(out_scores, lists, scores, lists)) ||
+      (out_positions != positions && overlap(out_positions, lists, positions, lists)))
+    return bad(fn, "out_scores and out_positions may be scores and positions, but must not overlap them otherwise");
+  if (overlap(out_scores, lists, positions, lists) || overlap(out_positions, lists, scores, lists) ||
+      overlap(out_scores, lists, out_positions, lists))
+    return bad(fn, "scores and positions must not share memory");
+  for (const void* p : {(const void*)scores, (const void*)positions, (const void*)out_scores, (const void*)out_positions})
+    if (overlap(out_len, lens, p, lists)) return bad(fn, "out_len must not lie in another array");
+  if (overlap(seq_len, lens, out_scores, lists) || overlap(seq_len, lens, out_positions, lists))
+    return bad(fn, "seq_len must not lie in an output");
   if (!workspace || !aligned16(workspace) || workspace_bytes < rtp_paged_evict_workspace(kv, stride))
     return bad(fn, "the workspace is missing, misaligned or smaller than rtp_paged_evict_workspace says");
   a.row_bytes = kv->head_dim * elem_size(kv->dtype);

@@ -30,3 +30,31 @@ def test_take_errors_refusals(lib):
     for kv, bits in ((_kv(err=None), BASE), (_kv(), None), (_kv(page_size=8), BASE)):
         assert lib.rtp_paged_take_errors(C.byref(kv), bits, None) == rtp.RTP_EINVAL
         assert rtp.rtp_last_error(None).startswith("rtp_paged_take_errors")
+
+
+FAR = 1 << 30  # between the arrays: each of three sequences, two heads and 80 slots is 1920 bytes
+
+
+def _evict(lib, **kw):
+    a = dict(lens=BASE, budget=20, recent=4, sink=2, scores=2 * FAR, pos=3 * FAR, stride=80, os=4 * FAR, op=5 * FAR, ol=6 * FAR,
+             ws=7 * FAR, wb=8, st=None)
+    a.update(kw)
+    return lib.rtp_paged_evict(C.byref(_kv()), *a.values())
+
+
+def test_evict_refuses_arrays_that_share_memory(lib):
+    """The heads' CTAs would write what others still read; a call in place is none of these.  (The
+    workspace given is too small: what passes ends there.)"""
+    def why(**kw):
+        assert _evict(lib, **kw) == rtp.RTP_EINVAL
+        return rtp.rtp_last_error(None)
+
+    small = why()
+    assert "workspace" in small
+    for ok in (dict(os=2 * FAR, op=3 * FAR), dict(os=2 * FAR), dict(op=3 * FAR), dict(os=2 * FAR + 1920), dict(ol=BASE + 12)):
+        assert why(**ok) == small, ok
+    for bad in (dict(ol=BASE), dict(ol=BASE + 8), dict(os=2 * FAR + 4), dict(os=2 * FAR - 1916), dict(op=3 * FAR + 1916),
+                dict(os=3 * FAR), dict(op=2 * FAR), dict(op=4 * FAR + 320), dict(ol=2 * FAR + 64), dict(ol=3 * FAR),
+                dict(ol=4 * FAR + 1912), dict(ol=5 * FAR - 8), dict(lens=4 * FAR), dict(lens=5 * FAR + 640)):
+        got = why(**bad)
+        assert got != small and ("must not" in got), (bad, got)
