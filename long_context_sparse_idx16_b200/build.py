@@ -1,6 +1,8 @@
-"""Build librtp.so (the CUDA library behind include/rtp.h and rtp_paged.h) in-tree for sm_100a, and
-_paged.so, the torch binding of the paged-cache operators."""
+"""Build librtp.so (the CUDA library behind include/rtp.h and rtp_paged.h) in-tree for sm_100a, and,
+where torch is installed, _paged.so, the torch binding of the paged-cache operators."""
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
@@ -11,6 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librtp.so")
 EXT = os.path.join(PKG, "_paged.so")
+EXT_FOR = os.path.join(PKG, "_paged.torch")  # what the binding was built for: it uses torch's internals
 EXT_SOURCE = os.path.join(CSRC, "paged_torch.cpp")
 CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -37,10 +40,23 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build_binding(force: bool = False) -> str:
-    """The torch binding: links to librtp.so beside it and to torch."""
+def _torch() -> str:
+    """The torch and the interpreter that a binding is for; empty without torch."""
+    if importlib.util.find_spec("torch") is None:
+        return ""
+    return f"torch {importlib.metadata.version('torch')} {sys.implementation.cache_tag}\n"
+
+
+def build_binding(force: bool = False):
+    """The torch binding: links to librtp.so beside it and to torch.  None without torch: the C
+    library does without it."""
+    built_for = _torch()
+    if not built_for:
+        print("torch is not installed: PagedKV's binding is not built", file=sys.stderr)
+        return None
     deps = [EXT_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(EXT) and all(os.path.getmtime(d) <= os.path.getmtime(EXT) for d in deps):
+    if (not force and os.path.exists(EXT) and os.path.exists(EXT_FOR) and open(EXT_FOR).read() == built_for
+            and all(os.path.getmtime(d) <= os.path.getmtime(EXT) for d in deps)):
         return EXT
     import sysconfig
 
@@ -56,6 +72,8 @@ def build_binding(force: bool = False) -> str:
         cmd += ["-L", d]
     cmd += ["-lc10", "-lc10_cuda", "-lcudart", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     subprocess.check_call(cmd)
+    with open(EXT_FOR, "w") as f:
+        f.write(built_for)
     return EXT
 
 

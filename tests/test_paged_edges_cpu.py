@@ -58,3 +58,39 @@ def test_evict_refuses_arrays_that_share_memory(lib):
                 dict(ol=4 * FAR + 1912), dict(ol=5 * FAR - 8), dict(lens=4 * FAR), dict(lens=5 * FAR + 640)):
         got = why(**bad)
         assert got != small and ("must not" in got), (bad, got)
+
+
+# ---------------------------------------------------------------- building
+
+
+@pytest.fixture
+def binding(tmp_path, monkeypatch):
+    """build_binding() in a folder of its own, with the compiler's calls recorded instead of run."""
+    calls = []
+
+    def run(cmd):
+        calls.append(cmd)
+        open(rtp_build.EXT, "w").close()
+
+    monkeypatch.setattr(rtp_build, "EXT", str(tmp_path / "_paged.so"))
+    monkeypatch.setattr(rtp_build, "EXT_FOR", str(tmp_path / "_paged.torch"))
+    monkeypatch.setattr(rtp_build.subprocess, "check_call", run)
+    return calls
+
+
+def test_library_builds_without_torch(lib, binding, monkeypatch, capsys):
+    import sys
+
+    monkeypatch.setitem(sys.modules, "torch", None)  # an import of it fails
+    assert rtp_build.build() == rtp_build.LIB
+    assert not binding and "torch is not installed" in capsys.readouterr().err
+
+
+def test_binding_is_rebuilt_for_another_torch(lib, binding, monkeypatch):
+    rtp_build.build()
+    rtp_build.build()
+    assert len(binding) == 1
+    monkeypatch.setattr(rtp_build.importlib.metadata, "version", lambda name: "0.0")
+    rtp_build.build()
+    rtp_build.build()
+    assert len(binding) == 2
