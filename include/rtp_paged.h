@@ -102,7 +102,8 @@ rtp_status rtp_paged_append(const rtp_paged_kv* kv, const void* q, const void* k
                             int64_t slot_pos_stride, cudaStream_t stream);
 
 /* Recompute kv->bounds of every page that holds one of the first seq_len[b] slots of a sequence,
- * from those slots' keys. */
+ * from those slots' keys.  Sequences that share a page must use it to the same slot (as they do a
+ * full page of a common prefix): each writes the bounds of what it uses. */
 rtp_status rtp_paged_bounds(const rtp_paged_kv* kv, const int32_t* seq_len, cudaStream_t stream);
 
 /* Attention of query rows over their sequences' pages:

@@ -74,6 +74,7 @@ class PagedKV(_paged.PagedKV):
 
     update_bounds(seq_lens, *, stream=None)
         Recompute the page bounds of every sequence's first seq_lens[b] slots from the stored keys.
+        Sequences that share a page must use it to the same slot.
     """
 
     def check(self, stream=None) -> None:
