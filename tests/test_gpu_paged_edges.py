@@ -87,6 +87,25 @@ def test_accumulated_weights_of_far_scores(kv, q, z, other, n):
     assert np.all(np.abs(f64(scores)[0, 0] - want) <= tol), (f64(scores)[0, 0][[7, 100, n - 3]], want[[7, 100, n - 3]])
 
 
+@pytest.mark.parametrize("kv,q", [("fp16", "fp16"), ("e4m3", "fp16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("gap", [18.0, 20.0])
+def test_small_weights_make_the_output(kv, q, gap):
+    """The one key that carries nearly all the weight has a value of zero: what is left are 39999 keys
+    of weights e^-18 and e^-20, which fp16 would round to 0 or to one step without their factor 2^15."""
+    n = 40000
+    c = Case([n], hq=4, hkv=1, d=64, page=64, kv=kv, q=q, seed=9)
+    x = torch.zeros(1, 4, 64, dtype=c.qt, device=c.device)
+    x[..., 0] = 8.0
+    k, v = torch.zeros(c.pool, 1, 64, 64), torch.ones(c.pool, 1, 64, 64)
+    v += torch.arange(64) / 64 * (kv == "fp16")
+    at = int(c.table[0, 300])
+    k[at, 0, 11, 0], v[at, 0, 11] = gap, 0.0
+    c.k, c.v = c.put(k), c.put(v)
+    out, lse = c.cache().decode(x, c.ints([n]), sm_scale=0.125, return_lse=True)
+    check_decode(c, x, out, lse, [(0, np.arange(n))], scale=0.125)
+    assert float(out.float().min()) > 0.5 * (n - 1) * math.exp(-gap)
+
+
 # ---------------------------------------------------------------- e4m3 pages under queries of any size
 
 
@@ -108,6 +127,98 @@ def test_e4m3_queries_at_the_ends_of_bf16(top):
 
 
 # ---------------------------------------------------------------- append
+
+
+def rotated(x, w, pos, eps, base):
+    """fp64 norm and rotation of [T][H][d], and the magnitude that its rounding errors scale with."""
+    d = x.shape[-1]
+    y = x if w is None else x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * w
+    a = np.asarray(pos, dtype=np.float64)[:, None, None] * base ** (-2.0 * np.arange(d // 2) / d)
+    y0, y1 = y[..., :d // 2], y[..., d // 2:]
+    mag = np.abs(y0) + np.abs(y1)
+    return np.concatenate([y0 * np.cos(a) - y1 * np.sin(a), y1 * np.cos(a) + y0 * np.sin(a)], -1), np.concatenate([mag, mag], -1)
+
+
+def close(got, want, mag, dtype, what):
+    """Half a step of the stored type, and 2^-19 of |y0| + |y1| for the fp32 arithmetic before it: the
+    norm's sum of d squares, root and products (2^-20), sine and cosine (reduced angle to 2^-24 pi,
+    two steps of sincosf)."""
+    tol = U[dtype] * np.abs(want) * 1.01 + 2.0**-19 * mag + TINY[dtype]
+    err = np.abs(got - want)
+    assert np.all(err <= tol), (what, float((err / tol).max()))
+
+
+def check_append(kv, q, d, page, new, hq, hkv, lens, norm="qk", give_q=True, in_place=False, seed=0):
+    """A chunk of new[b] tokens for each sequence, all that it writes against the definition, and the
+    rest of the pages left as they were."""
+    c = Case(lens, hq=hq, hkv=hkv, d=d, page=page, kv=kv, q=q, room=max(new) + 1, seed=seed,
+             **(dict(k_scale=0.0625, v_scale=0.03125) if kv == "e4m3" else {}))
+    T, eps, base = sum(new), 1e-5, 1e4
+    qkv = c.randn(T, hq + 2 * hkv, d, std=1.5).to(c.qt).to(c.device)
+    qn, kn, vn = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    q64, k64 = f64(qn), f64(kn)
+    w = {x: (1 + 0.2 * c.randn(d)).to(c.qt).to(c.device) if x in norm else None for x in "qk"}
+    bounds = torch.zeros((c.pool, hkv, 2, d), device=c.device).to(c.kt)
+    slots = torch.full((len(lens), hkv, c.width * page), -1, dtype=torch.int32, device=c.device)
+    old = {x: f64(getattr(c, x)) for x in "kv"}
+    cache = c.cache(bounds=bounds)
+    cache.update_bounds(c.ints(lens))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    out = cache.append(qn if give_q else None, kn, vn, c.ints(lens), cu_new=c.ints(cu), max_new=max(new), q_weight=w["q"],
+                       k_weight=w["k"], eps=eps, rope_base=base, q_out=qn if in_place else None, slot_positions=slots)
+    cache.check()
+    seq = np.repeat(np.arange(len(new)), new)
+    pos = np.asarray(lens)[seq] + np.arange(T) - cu[seq]
+    if give_q:
+        assert out is qn or not in_place
+        want, mag = rotated(q64, None if w["q"] is None else f64(w["q"]), pos, eps, base)
+        close(f64(out), want, mag, c.qt, "q")
+    else:
+        assert out is None
+    want, mag = rotated(k64, None if w["k"] is None else f64(w["k"]), pos, eps, base)
+    p, o = c.table.numpy()[seq, pos // page], pos % page
+    got = {x: f64(getattr(c, x)) for x in "kv"}
+    close(got["k"][p, :, o], want / c.k_scale, mag / c.k_scale, c.kt, "k")
+    close(got["v"][p, :, o], f64(vn) / c.v_scale, 0.0, c.kt, "v")
+    lim, ends = f64(bounds), np.asarray(lens) + np.asarray(new)
+    for b in range(len(lens)):  # each page's bounds are those of what it holds now
+        for i in range(-(-int(ends[b]) // page)):
+            rows = got["k"][int(c.table[b, i]), :, :min(page, int(ends[b]) - i * page)]
+            assert np.array_equal(lim[int(c.table[b, i]), :, 0], rows.min(1)), (b, i)
+            assert np.array_equal(lim[int(c.table[b, i]), :, 1], rows.max(1)), (b, i)
+    for x in "kv":
+        old[x][p, :, o] = got[x][p, :, o]
+        assert np.array_equal(got[x], old[x], equal_nan=True)
+    sp = np.full(slots.shape, -1)
+    sp[seq, :, pos] = pos[:, None]
+    assert np.array_equal(slots.cpu().numpy(), sp)
+
+
+# Row groups of a token (D / 16 lanes a row, 32 lanes a group) and the run of them that a warp takes:
+# the fewer tokens, the shorter, while 2368 warps are not reached.
+LARGE = [
+    (128, 32, 4, [3000]),            # 10 groups, all in one run
+    (128, 32, 4, [1, 0, 1499]),      # runs of 5: q alone, then q, k and v
+    (128, 32, 4, [350, 350]),        # runs of 3, the last of 1
+    (128, 32, 4, [480]),             # runs of 2
+    (64, 6, 1, [3001]),              # 3 groups, all in one run
+    (64, 6, 1, [700, 601, 0]),       # runs of 2 and 1
+    (64, 24, 3, [2400]),             # 5 groups, partly filled ones among them
+    (128, 6, 3, [1190, 3]),          # 4 groups, runs of 2
+]
+
+
+@pytest.mark.parametrize("kv,q", TYPES)
+@pytest.mark.parametrize("d,hq,hkv,new", LARGE)
+def test_append_large_chunks(kv, q, d, hq, hkv, new):
+    check_append(kv, q, d, 64 if d == 128 else 16, new, hq, hkv, [0, 63, 1000][:len(new)], seed=sum(new))
+
+
+@pytest.mark.parametrize("new", [[5, 0, 40], [1500, 2, 1000]])
+@pytest.mark.parametrize("norm,give_q,in_place", [("qk", True, True), ("q", True, False), ("k", True, True), ("k", False, False),
+                                                  ("", True, True)])
+def test_append_norms_in_place_and_without_queries(new, norm, give_q, in_place):
+    check_append("bf16", "bf16", 128, 32, new, 32, 4, [10, 0, 77], norm, give_q, in_place, seed=len(norm))
 
 
 def chunk(c, T):
@@ -385,3 +496,47 @@ def test_errors_are_taken_once_and_none_is_lost():
                 heard += 1
         assert heard >= 1, i
         cache.check()
+
+
+def test_calls_from_two_threads():
+    """Two threads with a stream each on one cache: every result is the one that a single thread gets."""
+    import threading
+
+    c = Case([4000, 900, 17], hq=8, hkv=2, d=128, page=64, kv="fp16", seed=71)
+    lens = c.ints(c.lens)
+    cache = c.cache(bounds=torch.zeros((c.pool, 2, 2, 128), dtype=c.kt, device=c.device))
+    cache.update_bounds(lens)
+    qs = [c.randn(3, 8, 128).to(c.qt).to(c.device) for _ in range(2)]
+
+    def step(q, **kw):
+        pages = cache.select_pages(q, lens, 9, n_first=1, **kw)
+        return cache.decode(q, lens, **kw), cache.decode(q, lens, pages=pages, **kw), pages[0]
+
+    want = [step(q) for q in qs]
+    torch.cuda.synchronize()
+    got, streams = [[], []], [torch.cuda.Stream() for _ in range(2)]
+
+    def work(i):
+        for _ in range(40):
+            got[i].append(step(qs[i], stream=streams[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert len(g) == 40
+        assert all(torch.equal(a, b) for r in g for a, b in zip(w, r))
+    cache.check()
+
+
+@pytest.mark.parametrize("kv,q,d,group", [("fp16", "fp16", 128, 12), ("bf16", "bf16", 128, 17), ("e4m3", "bf16", 128, 16),
+                                          ("e4m3", "fp16", 64, 8), ("e4m3", "bf16", 64, 3), ("bf16", "bf16", 64, 5),
+                                          ("fp16", "fp16", 64, 16)])
+def test_decode_long_rows_of_wide_groups_and_short_heads(kv, q, d, group):
+    """Long sequences split over many CTAs, in the builds for more than eight heads and for head dim 64."""
+    c = Case([12345, 0, 30001], hq=group, hkv=1, d=d, page=64, kv=kv, q=q, seed=group,
+             **(dict(k_scale=0.0625, v_scale=0.03125) if kv == "e4m3" else {}))
+    x = c.randn(3, group, d, std=2.0).to(c.qt).to(c.device)
+    out, lse = c.cache().decode(x, c.ints(c.lens), return_lse=True)
+    check_decode(c, x, out, lse, [(b, np.arange(n)) for b, n in enumerate(c.lens)])
