@@ -192,9 +192,10 @@ class PagedKV {
     if (pages) {
       const Tensor& p = pages->first;
       is(p, "pages", at::kInt);
-      if (p.dim() != 3 || p.size(0) != n || p.size(1) != h_.n_kv_heads || !p.is_contiguous())
-        bad("pages: expected contiguous indexes [", std::to_string(n), "][", std::to_string(h_.n_kv_heads), "][...], got ",
-            shape_of(p));
+      // (an empty list has no address, and without one every slot is attended)
+      if (p.dim() != 3 || p.size(0) != n || p.size(1) != h_.n_kv_heads || p.size(2) < 1 || !p.is_contiguous())
+        bad("pages: expected contiguous indexes [", std::to_string(n), "][", std::to_string(h_.n_kv_heads),
+            "][at least 1], got ", shape_of(p));
       exact(pages->second, "page counts", {n, h_.n_kv_heads}, at::kInt);
       ss = p.size(2);
       sel = p.data_ptr<int32_t>();

@@ -60,6 +60,27 @@ def test_evict_refuses_arrays_that_share_memory(lib):
         assert got != small and ("must not" in got), (bad, got)
 
 
+# ---------------------------------------------------------------- the binding
+
+
+def _cache():
+    k = torch.zeros((10, 2, 16, 64), dtype=torch.float16)
+    return rtp.PagedKV(k, k, torch.zeros((3, 5), dtype=torch.int32), bounds=torch.zeros((10, 2, 2, 64), dtype=torch.float16))
+
+
+def _ints(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def test_page_lists_of_no_pages_are_refused():
+    """They were taken for no list at all: attention to every slot."""
+    q = torch.zeros((3, 4, 64), dtype=torch.float16)
+    with pytest.raises(ValueError, match="at least 1"):
+        _cache().decode(q, _ints(3), pages=(_ints(3, 2, 0), _ints(3, 2)))
+    with pytest.raises(ValueError, match="CUDA device"):  # the next thing that is looked at
+        _cache().decode(q, _ints(3), pages=(_ints(3, 2, 1), _ints(3, 2)))
+
+
 # ---------------------------------------------------------------- building
 
 
