@@ -223,6 +223,7 @@ rtp_status rtp_paged_decode(const rtp_paged_kv* kv, const void* q, int32_t q_dty
   a.n_sink = window ? n_sink : 0;
   const float scale = sm_scale > 0.f ? sm_scale : (float)(1.0 / sqrt((double)kv->head_dim));
   a.scale_log2 = (float)((double)scale * kv->k_scale * 1.4426950408889634);
+  if (!isfinite(a.scale_log2)) return bad(fn, "sm_scale * k_scale must be below fp32's largest value by log2(e)");
   a.sel = sel;
   a.sel_count = sel_count;
   a.sel_stride = sel_stride;

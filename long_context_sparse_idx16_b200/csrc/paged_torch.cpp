@@ -187,6 +187,7 @@ class PagedKV {
                     OptTensor out, bool return_lse, const py::object& stream) {
     const int64_t qs = queries(q), n = q.size(0), hq = q.size(1);
     rows(n, seq_lens, row_seq);
+    if (sm_scale != 0.0 && (float)sm_scale == 0.f) bad("sm_scale is below fp32's least value (0 stands for 1/sqrt(D))");
     const int32_t *sel = nullptr, *cnt = nullptr;
     int64_t ss = 0, st = 0;
     if (pages) {

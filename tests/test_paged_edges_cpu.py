@@ -32,6 +32,23 @@ def test_take_errors_refusals(lib):
         assert rtp.rtp_last_error(None).startswith("rtp_paged_take_errors")
 
 
+def _decode(lib, kv, **kw):
+    a = dict(q=BASE, dtype=0, qs=256, rows=3, hq=4, seq=None, lens=BASE, window=0, sink=0, scale=0.0, sel=None, cnt=None,
+             ss=0, out=BASE, os=256, lse=None, scores=None, scs=0, ws=BASE, wb=0, st=None)
+    a.update(kw)
+    return lib.rtp_paged_decode(C.byref(kv), *a.values())
+
+
+def test_decode_refuses_scales_beyond_fp32(lib):
+    """Infinite, the product made every row NaN; as zero, it stood for the default."""
+    assert _decode(lib, _kv(k_scale=1e30), scale=1e30, wb=1 << 40) == rtp.RTP_EINVAL
+    assert "sm_scale" in rtp.rtp_last_error(None)
+    assert _decode(lib, _kv(k_scale=1e30), scale=1e-30) == rtp.RTP_EINVAL  # (passes, up to the workspace)
+    assert "workspace" in rtp.rtp_last_error(None)
+    with pytest.raises(ValueError, match="sm_scale"):
+        _cache().decode(torch.zeros((3, 4, 64), dtype=torch.float16), _ints(3), sm_scale=1e-50)
+
+
 FAR = 1 << 30  # between the arrays: each of three sequences, two heads and 80 slots is 1920 bytes
 
 
