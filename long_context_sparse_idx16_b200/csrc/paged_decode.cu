@@ -307,12 +307,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(mbar)
-               : "memory");
-}
-
 template <typename QT, typename K, int D, int NB>
 __global__ void __launch_bounds__(kThreads, per_sm(NB, D)) attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap km,
                                                                     const __grid_constant__ CUtensorMap vm) {

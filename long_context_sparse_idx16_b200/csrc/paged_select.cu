@@ -76,12 +76,6 @@ __device__ __forceinline__ Run run_at(const SelectPagesArgs& a, int r, int end) 
   return u;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(mbar)
-               : "memory");
-}
-
 // One CTA: a KV head, a block of rows, `rounds` times 128 pages.  The rows' queries are laid out in
 // shared memory in the order of the contraction, max(q, 0) and min(q, 0) apart; from there on the warps
 // work by themselves, 16 pages at a time.  A lane copies half of one page's bounds (its lo or its hi

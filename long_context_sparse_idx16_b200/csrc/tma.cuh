@@ -41,6 +41,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Untiled copy: both addresses and the size multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(mbar)
+               : "memory");
+}
+
 // Host: encode a tiled tensor map (no interleave, zero fill out of bounds).  dims/strides as
 // cuTensorMapEncodeTiled takes them: dims[0] innermost, strides[i] (bytes) for dims[i + 1].
 // Returns false (and leaves *map unspecified) if the driver refuses the description.
