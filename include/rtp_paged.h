@@ -92,8 +92,8 @@ rtp_status rtp_paged_take_errors(const rtp_paged_kv* kv, uint32_t* bits, cudaStr
  * q, k, v: DEVICE fp16 or bf16 (dtype; that of the pages unless those are e4m3), heads
  * contiguous, rows q_stride, k_stride, v_stride elements apart (multiples of 8).  q_out: rows
  * q_out_stride apart; it may be q itself.  q and q_out may both be NULL (n_q_heads is then
- * ignored).  max_new: about the most tokens of one sequence (sizes a launch).  A page written to
- * must belong to one sequence only. */
+ * ignored).  max_new: about the most tokens of one sequence (1 to n_tokens; sizes a launch).  A page
+ * written to must belong to one sequence only. */
 rtp_status rtp_paged_append(const rtp_paged_kv* kv, const void* q, const void* k, const void* v, int32_t dtype,
                             int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t n_tokens,
                             int32_t n_q_heads, const int32_t* cu_new, int32_t max_new, const int32_t* seq_len,
@@ -110,7 +110,8 @@ rtp_status rtp_paged_bounds(const rtp_paged_kv* kv, const int32_t* seq_len, cuda
  *     out[r][h] = softmax_j(sm_scale * q[r][h] . key_j) value_j,  h reads KV head h / (Hq / Hkv),
  * over slots j < row_len[r] of sequence row_seq[r] (NULL: row r reads sequence r).  A row with no
  * slot gives zeros and lse = -inf.
- *   window > 0: only slots j >= row_len - window or j < n_sink.
+ *   window > 0: only slots j >= row_len - window or j < n_sink.  (Slots, not positions: after an
+ *     eviction, which fills holes with later rows, they are not the last tokens.)
  *   sel != NULL: only the slots of the listed pages: sel DEVICE [n_rows][Hkv][sel_stride] page
  *     indexes of the sequence (not pool pages), sel_count DEVICE [n_rows][Hkv]; each page at most
  *     once (a repeated page counts twice); indexes outside the row's pages are skipped (-1 may pad
@@ -140,7 +141,8 @@ size_t rtp_paged_decode_workspace(const rtp_paged_kv* kv, int32_t n_rows, int32_
  * n_recent are always taken, then others in (score desc, page asc) order, min(top_pages, pages) in
  * all.  sel: DEVICE [n_rows][Hkv][sel_stride] receives their indexes ascending, then -1 up to
  * top_pages; sel_count: DEVICE [n_rows][Hkv].  Needs kv->bounds, n_first + n_recent <= top_pages
- * <= sel_stride.  A score that is not a number ranks last. */
+ * <= sel_stride.  A score that is not a number ranks last, and so does a page outside the pool, with
+ * RTP_PAGED_ERANGE, where there is a choice; where a page is taken without one it is not looked at. */
 rtp_status rtp_paged_select(const rtp_paged_kv* kv, const void* q, int32_t q_dtype, int64_t q_stride,
                             int32_t n_rows, int32_t n_q_heads, const int32_t* row_seq, const int32_t* row_len,
                             int32_t top_pages, int32_t n_first, int32_t n_recent, int32_t* sel, int64_t sel_stride,
@@ -157,8 +159,9 @@ size_t rtp_paged_select_workspace(const rtp_paged_kv* kv, int32_t n_rows, int32_
  * below it, in slot order: K and V rows, score, position; all other rows stay where they are, and
  * rows at and behind `budget` keep their bytes.  out_len[b] (DEVICE) = min(seq_len[b], budget);
  * out_scores and out_positions (may be scores and positions; no arrays share memory otherwise, so
- * out_len is not seq_len) receive slots 0 .. out_len - 1, then 0 and -1 up to stride.  budget and stride are at most 2^24.  Pages moved into keep their bounds;
- * call rtp_paged_bounds where those are in use.  A page must belong to one sequence only. */
+ * out_len is not seq_len) receive slots 0 .. out_len - 1, then 0 and -1 up to stride.  budget and
+ * stride are at most 2^24.  Pages moved into keep their bounds; call rtp_paged_bounds where those are
+ * in use.  A page must belong to one sequence only. */
 rtp_status rtp_paged_evict(const rtp_paged_kv* kv, const int32_t* seq_len, int32_t budget, int32_t n_recent,
                            int32_t n_sink, const float* scores, const int32_t* positions, int64_t stride,
                            float* out_scores, int32_t* out_positions, int32_t* out_len, void* workspace,

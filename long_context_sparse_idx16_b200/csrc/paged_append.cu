@@ -16,9 +16,9 @@
 // several rows: a second kernel takes its bounds from the rows just written (in L2: the other rows are
 // read and written as streams).
 //
-// Measured (one B200, 32 / 4 heads of 128, bf16, norms, bounds): 16384 tokens, 336 MB, in 69 us (4.9
-// TB/s), 60 us of it this kernel (5.6 TB/s of the 6.55 that a copy reaches); 64 tokens in 4 us.  Four
-// dims a lane instead of eight took 134 us (54.8 M warp instructions instead of 35.8 M).
+// Measured (one B200, 32 / 4 heads of 128, bf16, norms, bounds): 16384 tokens, 336 MB, in 70.6 us (4.8
+// TB/s); on inputs already in L2 65.6 us, 60.7 us of it this kernel; 64 tokens in 4 us.  Four dims
+// a lane instead of eight took 134 us (54.8 M warp instructions instead of 35.8 M).
 #include "paged.cuh"
 
 namespace rtp {

@@ -21,17 +21,21 @@
 //     heads as the columns: S^T = K Q^T, O^T = V^T P^T, the weights transposed by movmatrix.  A
 //     tcgen05 tile (64 or 128 rows) would be mostly padding, and the tensor pipe is not the bound.
 //   * Scores, maxima, sums and outputs are fp32.  The weights are rounded once to 16 bits for the
-//     product with the values; in fp16 they carry a factor 2^15, so that weights down to 2^-29 of
-//     the largest keep all their bits and sums of many small ones are not lost.
+//     product with the values, to the type of these (mma.sync takes both operands in one): by at most
+//     half a step each, and independently, so that over many keys the output's own rounding is the
+//     larger (the error against 64 bits grows by up to 11%).  Keeping more bits would take a second
+//     product with the remainders.  In fp16 the weights carry a factor 2^15, so that those down to
+//     2^-29 of the largest keep all their bits and sums of many small ones are not lost.
 //   * e4m3 pages are read as 16-bit pairs and widened to fp16 (exactly): ldmatrix gives a lane four
 //     successive dims of a key, which the query fragments match by the same permutation of the
 //     contraction, and (transposed) two dims of two keys, which a byte permute splits over two
 //     output rows.  Their queries are scaled per head by a power of two into fp16's range, which is
 //     exact for values down to 2^-29 of the head's largest and off by 2^-40 of that below.
 // Measured (one B200, 32 / 4 heads of 128; a copy reaches 6.55 TB/s): 8 x 128K fp16 keys, 2.15 GB, in
-// 326 us (6.6 TB/s); 1M e4m3 keys, 1.07 GB, in 185 us (5.8 TB/s; the widening keeps the issue slots
-// half busy); 48 sequences of 1 to 32K keys, 363 MB, in 70 us (5.2 TB/s, of which 10 us are starts,
-// ends and the join); 777 keys in 9 us, latency.  Sixteen query rows to a tile (queries as the rows)
+// 326 us (6.6 TB/s); 1M e4m3 keys, 1.07 GB, in 188 us (5.7 TB/s; the widening keeps the issue slots
+// half busy; 178 us on the same cache again and again, where L2 holds a part); 48 sequences of 1 to 32K
+// keys, 363 MB, in 69 us (5.2 TB/s, of which 10 us are starts, ends and the join); 777 keys in 9 us,
+// latency.  A window of 8192 and 4 sinks of 8 x 128K keys, 134 MB, 32 us.  Sixteen query rows to a tile (queries as the rows)
 // took 254 us at 1M e4m3 keys; unweighted problems took 132 us for the 48 sequences.
 // Accumulated weights need the final sums: the scores go through the workspace in fp32 and
 // weights_kernel adds exp2((s - M) - log2 L) over the query heads, beside the join.

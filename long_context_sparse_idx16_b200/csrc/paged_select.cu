@@ -3,10 +3,12 @@
 // For KV head g: score(page) = max_h sum_d max(q_hd lo_d, q_hd hi_d) over g's query heads h, which is
 // [max(q, 0), min(q, 0)] . [hi, lo]: a product with 2 D terms.  The top pages by the exact (fp64)
 // scores are wanted, ties to the lower page; that takes two steps:
-//   * page_score_kernel forms all scores on the tensor cores (mma.sync, fp32 sums).  Products of
-//     16-bit values are exact, so a score is off by at most eps = 2^-14 |q|_1 max|bound|: 2 D / 16
-//     steps that each add 16 products and the running sum, every term cut at 2^-23 of the largest,
-//     make at most 16 * 17 * 2^-23 < 2^-14.9 of the sum of all magnitudes.
+//   * page_score_kernel forms all scores on the tensor cores (mma.sync, fp32 sums) and takes them to be
+//     off by at most eps = 2^-14 |q|_1 max|bound|.  How these instructions add is not documented.  The
+//     assumption is: products of 16-bit values exact; 2 D / 16 steps that each add 16 products and
+//     the running sum, every term cut at 2^-23 of the largest, which make at most 16 * 17 * 2^-23 <
+//     2^-14.9 of the sum of all magnitudes; 2^-14 leaves a factor 1.9.  Tests of scores nearer to one
+//     another than fp32 tells check the choice.
 //   * page_pick_kernel finds the bin of the last page taken in a linear histogram of these scores.
 //     Pages above the bin by 2 eps are in, pages below it by 2 eps are out; the few between get
 //     their exact fp64 scores and are ranked by them.  Where too many are between (equal scores,

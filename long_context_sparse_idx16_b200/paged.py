@@ -52,7 +52,8 @@ class PagedKV(_paged.PagedKV):
            out=None, return_lse=False, stream=None)
         Attention of query rows over their sequences' pages.  q: [rows][Hq][D]; row r attends to the
         first seq_lens[r] slots of sequence row_seq[r] (default: sequence r).  window > 0 keeps the
-        last `window` slots and the first n_sink.  pages: (indexes, counts) from ``select_pages``
+        last `window` slots and the first n_sink (slots, not positions: after ``evict`` they are not
+        the last tokens).  pages: (indexes, counts) from ``select_pages``
         keeps those pages alone.  scores: fp32 [n_seqs][Hkv][S], to which each slot's weight, summed
         over the KV head's queries, is added.  sm_scale 0: 1/sqrt(D).  Returns out ([rows][Hq][D],
         q's dtype) and, with return_lse, also the fp32 [rows][Hq] natural log-sum-exp.  A row
