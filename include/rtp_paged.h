@@ -43,7 +43,7 @@ extern "C" {
 typedef enum { RTP_FP16 = 0, RTP_BF16 = 1, RTP_E4M3 = 2 } rtp_dtype;
 
 /* Bits of rtp_paged_kv.err */
-#define RTP_PAGED_ERANGE 2u   /* a page, length or sequence number out of range was left out */
+#define RTP_PAGED_ERANGE 2u   /* a page, length, sequence or row number out of range was left out */
 #define RTP_PAGED_ETIMEOUT 4u /* a bounded in-kernel wait gave up; results of that call are invalid */
 
 /* A paged cache of one layer.  Element (page, head, slot, d) of k lies at
@@ -71,7 +71,7 @@ typedef struct {
 } rtp_paged_kv;
 
 /* Move kv->err to *bits (DEVICE) and clear it, in one step: an error that another stream reports
- * meanwhile is in this answer or in the next. */
+ * meanwhile is in this answer or in the next.  Of kv only err is looked at. */
 rtp_status rtp_paged_take_errors(const rtp_paged_kv* kv, uint32_t* bits, cudaStream_t stream);
 
 /* Append new tokens.  Token t of sequence b is row cu_new[b] + i of q, k and v (cu_new DEVICE

@@ -101,7 +101,10 @@ const char* check_rows(const rtp_paged_kv* kv, const void* q, int64_t q_stride, 
   return nullptr;
 }
 
-__global__ void take_errors_kernel(uint32_t* err, uint32_t* bits) { *bits = atomicExch(err, 0u); }
+__global__ void take_errors_kernel(uint32_t* err, uint32_t* bits) {
+  after_wait();
+  *bits = atomicExch(err, 0u);
+}
 
 }  // namespace
 
@@ -109,10 +112,8 @@ extern "C" {
 
 rtp_status rtp_paged_take_errors(const rtp_paged_kv* kv, uint32_t* bits, cudaStream_t stream) {
   const char* fn = "rtp_paged_take_errors";
-  if (const char* m = view_of(kv, nullptr)) return bad(fn, m);
-  if (!kv->err || !bits) return bad(fn, "kv->err and bits must not be NULL");
-  take_errors_kernel<<<1, 1, 0, stream>>>(kv->err, bits);
-  const cudaError_t e = cudaGetLastError();
+  if (!kv || !kv->err || !bits) return bad(fn, "kv, kv->err and bits must not be NULL");
+  const cudaError_t e = launch_after(take_errors_kernel, dim3(1), 1, 0, stream, kv->err, bits);
   return e == cudaSuccess ? RTP_OK : cuda_fail(nullptr, e, fn);
 }
 

@@ -35,8 +35,9 @@
 // 326 us (6.6 TB/s); 1M e4m3 keys, 1.07 GB, in 188 us (5.7 TB/s; the widening keeps the issue slots
 // half busy; 178 us on the same cache again and again, where L2 holds a part); 48 sequences of 1 to 32K
 // keys, 363 MB, in 69 us (5.2 TB/s, of which 10 us are starts, ends and the join); 777 keys in 9 us,
-// latency.  A window of 8192 and 4 sinks of 8 x 128K keys, 134 MB, 32 us.  Sixteen query rows to a tile (queries as the rows)
-// took 254 us at 1M e4m3 keys; unweighted problems took 132 us for the 48 sequences.
+// latency.  A window of 8192 and 4 sinks of 8 x 128K keys, 134 MB, in 32 us.  Sixteen query rows to a
+// tile (queries as the rows) took 254 us at 1M e4m3 keys; unweighted problems took 132 us for the 48
+// sequences.
 // Accumulated weights need the final sums: the scores go through the workspace in fp32 and
 // weights_kernel adds exp2((s - M) - log2 L) over the query heads, beside the join.
 #include <type_traits>

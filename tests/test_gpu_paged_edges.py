@@ -540,3 +540,14 @@ def test_decode_long_rows_of_wide_groups_and_short_heads(kv, q, d, group):
     x = c.randn(3, group, d, std=2.0).to(c.qt).to(c.device)
     out, lse = c.cache().decode(x, c.ints(c.lens), return_lse=True)
     check_decode(c, x, out, lse, [(b, np.arange(n)) for b, n in enumerate(c.lens)])
+
+
+def test_check_of_a_cache_that_calls_refuse():
+    """A cache of a page size that no call takes has met no error."""
+    from long_context_sparse_idx16_b200 import PagedKV, RTPError
+
+    k = torch.zeros((3, 1, 24, 64), dtype=torch.float16, device="cuda")
+    cache = PagedKV(k, k, torch.zeros((1, 2), dtype=torch.int32, device="cuda"))
+    with pytest.raises(RTPError, match="page_size"):
+        cache.decode(torch.zeros((1, 2, 64), dtype=torch.float16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"))
+    cache.check()
